@@ -498,6 +498,122 @@ tp_status tp_mlp_block_backward_recompute(const void* X, const void* W1, const v
 size_t tp_mlp_block_backward_recompute_workspace_size(int64_t T, int64_t d, int64_t k, int p,
                                                       int act);
 
+/* ------------------------------------------------------------------------
+ * Positions, head norms and scored attention: the steps between the Q, K, V
+ * projections and the output projection of a block whose attention knows
+ * positions.  The pages stop at softmax(Q K^T / sqrt(d_k)) V per head
+ * ("Tensor parallel math", "Attention: parallel across heads"); these calls
+ * act on each shard's own heads as tp_attention_heads does, with no
+ * communication, on the same layouts:
+ *   queries      [p][T][(n_heads/p) * head_dim]
+ *   keys, values [p][T][(n_kv_heads/p) * head_dim]
+ */
+
+typedef enum {
+  TP_ROPE_HALF = 0,        /* pair i: elements i and i + rotary_dim/2       */
+  TP_ROPE_INTERLEAVED = 1  /* pair i: elements 2i and 2i + 1                */
+} tp_rope_layout;
+
+/* Long-context scaling of the frequencies w_i = base^(-2i/r), r = rotary_dim: */
+typedef enum {
+  TP_ROPE_SCALE_NONE = 0,
+  TP_ROPE_SCALE_LINEAR = 1, /* w_i / factor                                  */
+  TP_ROPE_SCALE_BASE = 2,   /* base * factor^(r/(r-2)) in place of base      */
+  TP_ROPE_SCALE_BANDS = 3,  /* by turns n_i = original_len w_i / 2 pi: w_i
+                               from `high` turns up, w_i / factor up to `low`
+                               turns, linear in n_i between                  */
+  TP_ROPE_SCALE_RAMP = 4    /* by pair index: w_i up to the pair that turns
+                               `high` times in original_len (rounded down),
+                               w_i / factor from the one that turns `low`
+                               times (rounded up), linear in i between       */
+} tp_rope_scaling;
+
+typedef struct tp_rope_config {
+  int rotary_dim;       /* rotated leading elements of a head: even, 2..256   */
+  int layout;           /* tp_rope_layout                                     */
+  int scaling;          /* tp_rope_scaling                                    */
+  double base;          /* > 1                                                */
+  double factor;        /* >= 1; read when scaling is not NONE                */
+  double original_len;  /* > 0; read for BANDS and RAMP                       */
+  double low, high;     /* 0 < low < high; read for BANDS and RAMP            */
+  double amplitude;     /* > 0: factor on every sine and cosine; 0: 1, and
+                           0.1 ln(factor) + 1 for RAMP                        */
+} tp_rope_config;
+
+#define TP_ROPE_MAX_PAIRS 128
+
+/* A rotation's plan: host data, filled by tp_rope_plan_init and passed by
+ * address (copied by each call; nothing of it lives on the device). */
+typedef struct tp_rope_plan {
+  int rotary_dim, layout;
+  float amplitude;
+  int reserved;
+  uint64_t turn[TP_ROPE_MAX_PAIRS]; /* w_i / 2 pi in units of 2^-64 turns */
+} tp_rope_plan;
+
+tp_status tp_rope_plan_init(const tp_rope_config* config, tp_rope_plan* plan);
+
+/*
+ * Rotary positions.  Every head's pairs (x1, x2) of its first rotary_dim
+ * elements turn by the angle f = position * w_i:
+ *   (x1, x2) -> amplitude * (x1 cos f - x2 sin f, x2 cos f + x1 sin f);
+ * the elements behind them are copied.  The angle is reduced exactly (64-bit
+ * fractions of a turn), so positions anywhere in int32 are as good as small
+ * ones.  `inverse` nonzero turns by -f: the transpose, i.e. the backward
+ * pass (dQ from dQout).
+ *
+ *   Q, Q_out   [p][T][(n_heads/p) * head_dim]     dtype
+ *   K, K_out   [p][T][(n_kv_heads/p) * head_dim]  dtype; Q and Q_out, or K
+ *              and K_out, may both be NULL (its head count is then ignored)
+ *   positions  [T] int32 device, the same for every shard and head; NULL: t
+ * An output may be its input's own buffer (in place); any other overlap of
+ * an output with a buffer of the call is TP_ERR_INVALID_ARG.  head_dim 2..256
+ * (else TP_ERR_UNSUPPORTED), rotary_dim <= head_dim.  Buffers are aligned to
+ * their element, else TP_ERR_ALIGNMENT; with head_dim and rotary_dim
+ * multiples of 16 and 16-byte aligned buffers the accesses are vectors.
+ */
+tp_status tp_rope(const void* Q, const void* K, const int32_t* positions, void* Q_out, void* K_out,
+                  int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                  const tp_rope_plan* plan, tp_dtype dtype, int inverse, void* stream);
+
+/*
+ * Norm of every query and key head with the rotation in the same pass:
+ *   y = rotate(x * rstd * w),  rstd = (mean(x^2) + eps)^(-1/2) over the head.
+ *   wq, wk  [head_dim] fp32, shared by all heads and shards; NULL: no weight
+ *   plan    NULL: the norm alone
+ *   eps     > 0
+ * Other arguments, in-place use and errors as in tp_rope.
+ */
+tp_status tp_qk_norm_rope(const void* Q, const void* K, const float* wq, const float* wk,
+                          const int32_t* positions, void* Q_out, void* K_out, int64_t T, int p,
+                          int n_heads, int n_kv_heads, int head_dim, const tp_rope_plan* plan,
+                          float eps, tp_dtype dtype, void* stream);
+
+/*
+ * Its backward.  With g the upstream gradient rotated back and xhat = x rstd:
+ *   dx = rstd (g w - xhat mean(g w xhat)),   dw = sum of g xhat over all
+ *   shards, tokens and heads (fp32, in a fixed order: reproducible).
+ *   Q, K            the forward call's inputs
+ *   dQ_out, dK_out  gradients of Q_out, K_out        dtype
+ *   dQ, dK          outputs, dtype; dQ may be dQ_out's buffer, dK dK_out's
+ *   dwq, dwk        [head_dim] fp32 outputs; NULL to skip
+ *   workspace       tp_qk_norm_rope_backward_workspace_size(...) bytes,
+ *                   256-byte aligned
+ * Either all of Q, dQ_out, dQ or all of K, dK_out, dK may be NULL; its dw is
+ * then set to zero.  T == 0 sets the given dw to zero and returns.
+ */
+tp_status tp_qk_norm_rope_backward(const void* Q, const void* K, const float* wq, const float* wk,
+                                   const int32_t* positions, const void* dQ_out,
+                                   const void* dK_out, void* dQ, void* dK, float* dwq, float* dwk,
+                                   void* workspace, size_t workspace_bytes, int64_t T, int p,
+                                   int n_heads, int n_kv_heads, int head_dim,
+                                   const tp_rope_plan* plan, float eps, tp_dtype dtype,
+                                   void* stream);
+
+/* Workspace bytes tp_qk_norm_rope_backward needs (0 if the arguments are invalid). */
+size_t tp_qk_norm_rope_backward_workspace_size(int64_t T, int p, int n_heads, int n_kv_heads,
+                                               int head_dim);
+
 /* Synchronise `stream`, then report (and clear) the device status word of
  * the current device: TP_ERR_DEVICE_TIMEOUT if a bounded wait ran out since
  * the last call, TP_ERR_CUDA if the stream reported an error, else TP_OK. */
@@ -542,10 +658,11 @@ uint64_t tp_kernel_launch_count(void);
 
 /* ABI version of this header (bumped on any signature change or added call;
  * 2: the p-GPU fold and IPC calls, the exp2 test hook, and a host-buffer
- * workspace sized for two chunks). */
+ * workspace sized for two chunks; 3: rotary positions, head norms and scored
+ * attention). */
 int tp_abi_version(void);
 
-#define TP_ABI_VERSION 2
+#define TP_ABI_VERSION 3
 
 #ifdef __cplusplus
 }

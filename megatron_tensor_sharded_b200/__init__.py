@@ -25,6 +25,12 @@ Example -- the MLP block on p = 4 simulated shards, bf16 in, fp32 out::
                     tp.TP_BF16, tp.TP_ACT_GELU_TANH)
     tp.tp_sync_status()          # raises TPError if a device wait timed out
 
+Positions and head norms act on the projections' outputs, [p][T][(h/p) * dh]::
+
+    plan = tp.rope_plan(rotary_dim=128, base=500000.0, scaling="bands", factor=8.0,
+                        original_len=8192, low=1.0, high=4.0)      # host data, made once
+    tp.tp_rope(Q, K, positions, Q, K, T, p, n_heads, n_kv_heads, 128, plan, tp.TP_BF16)
+
 The same pattern serves tp_attn_block, tp_transformer_block (weights in a
 BlockParams built by ``block_params(**tensors)``) and tp_mlp_block_backward.
 """
@@ -48,6 +54,10 @@ __all__ = [
     "tp_transformer_block_workspace_size", "tp_mlp_block_backward",
     "tp_mlp_block_backward_workspace_size", "tp_mlp_block_backward_recompute",
     "tp_mlp_block_backward_recompute_workspace_size",
+    # rotary positions and head norms
+    "ROPE_LAYOUT", "ROPE_SCALING", "RopeConfig", "RopePlan", "rope_plan", "tp_rope_plan_init",
+    "tp_rope", "tp_qk_norm_rope", "tp_qk_norm_rope_backward",
+    "tp_qk_norm_rope_backward_workspace_size",
     # the all-reduce of partials held on p GPUs
     "TP_GATHER_MAX", "IpcHandle", "tp_reduce_partials_gather", "tp_ipc_export", "tp_ipc_import",
     "tp_ipc_release",
@@ -65,6 +75,8 @@ TP_FLAG_NONE, TP_FLAG_SPLITK_FUSED, TP_FLAG_FUSED_LAUNCH, TP_FLAG_ROW_FOLD = 0, 
 DTYPE = {"f32": TP_F32, "bf16": TP_BF16}
 ACT = {"gelu_tanh": TP_ACT_GELU_TANH, "swiglu": TP_ACT_SWIGLU, "identity": TP_ACT_IDENTITY,
        "relu": TP_ACT_RELU}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 STATUS = {0: "TP_OK", 1: "TP_ERR_INVALID_ARG", 2: "TP_ERR_INDIVISIBLE", 3: "TP_ERR_ALIGNMENT",
           4: "TP_ERR_UNSUPPORTED", 5: "TP_ERR_CUDA", 6: "TP_ERR_DEVICE_TIMEOUT",
           7: "TP_ERR_WORKSPACE"}
@@ -100,6 +112,21 @@ class BlockParams(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in (
         "ln1_gamma", "ln1_beta", "Wq", "Wk", "Wv", "Wo", "bo", "ln2_gamma", "ln2_beta", "W1",
         "W_up", "b1", "W2", "b2")]
+
+
+class RopeConfig(ctypes.Structure):
+    """tp_rope_config: what a rotation's plan is made from."""
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class RopePlan(ctypes.Structure):
+    """tp_rope_plan: host data, passed by address and copied by each call."""
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int),
+                ("turn", ctypes.c_uint64 * 128)]
 
 
 def _load() -> ctypes.CDLL:
@@ -148,6 +175,14 @@ def _load() -> ctypes.CDLL:
     lib.tp_debug_exp2_poly.argtypes = [vp, vp, i64, vp]
     lib.tp_reduce_partials_gather.argtypes = [ctypes.POINTER(vp), i32, vp, ctypes.POINTER(vp), i32,
                                               i64, i64, i64, vp]
+    plan, f32 = ctypes.POINTER(RopePlan), ctypes.c_float
+    lib.tp_rope_plan_init.argtypes = [ctypes.POINTER(RopeConfig), plan]
+    lib.tp_rope.argtypes = [vp] * 5 + [i64, i32, i32, i32, i32, plan, i32, i32, vp]
+    lib.tp_qk_norm_rope.argtypes = [vp] * 7 + [i64, i32, i32, i32, i32, plan, f32, i32, vp]
+    lib.tp_qk_norm_rope_backward.argtypes = [vp] * 12 + [sz, i64, i32, i32, i32, i32, plan, f32,
+                                                         i32, vp]
+    lib.tp_qk_norm_rope_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    lib.tp_qk_norm_rope_backward_workspace_size.restype = sz
     lib.tp_ipc_export.argtypes = [vp, ctypes.POINTER(IpcHandle)]
     lib.tp_ipc_import.argtypes = [ctypes.POINTER(IpcHandle), ctypes.POINTER(vp)]
     lib.tp_ipc_release.argtypes = [ctypes.POINTER(IpcHandle)]
@@ -163,7 +198,8 @@ def _load() -> ctypes.CDLL:
               "tp_reduce_partials_residual", "tp_transformer_block", "tp_mlp_block_backward",
               "tp_mlp_block_backward_recompute", "tp_sync_status", "tp_abi_version",
               "tp_debug_exp2_poly", "tp_reduce_partials_gather", "tp_ipc_export",
-              "tp_ipc_import", "tp_ipc_release"):
+              "tp_ipc_import", "tp_ipc_release", "tp_rope_plan_init", "tp_rope",
+              "tp_qk_norm_rope", "tp_qk_norm_rope_backward"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -375,6 +411,52 @@ def tp_ipc_import(handle: IpcHandle) -> int:
 
 def tp_ipc_release(handle: IpcHandle) -> None:
     _check(_lib.tp_ipc_release(ctypes.byref(handle)), True)
+
+
+def tp_rope_plan_init(config: RopeConfig, plan: RopePlan, check=True):
+    return _check(_lib.tp_rope_plan_init(ctypes.byref(config), ctypes.byref(plan)), check)
+
+
+def rope_plan(rotary_dim=128, layout="half", base=10000.0, scaling="none", factor=1.0,
+              original_len=0.0, low=1.0, high=4.0, amplitude=0.0) -> RopePlan:
+    """A rotation's plan (tp_rope_config's fields; layout and scaling by name)."""
+    cfg = RopeConfig(rotary_dim, ROPE_LAYOUT[layout], ROPE_SCALING[scaling], base, factor,
+                     original_len, low, high, amplitude)
+    plan = RopePlan()
+    tp_rope_plan_init(cfg, plan)
+    return plan
+
+
+def tp_rope(Q, K, positions, Q_out, K_out, T, p, n_heads, n_kv_heads, head_dim, plan, dtype,
+            inverse=False, stream=None, check=True):
+    """Rotary positions of every shard's queries and keys; inverse=True turns
+    back (the backward pass)."""
+    return _check(_lib.tp_rope(_ptr(Q), _ptr(K), _ptr(positions), _ptr(Q_out), _ptr(K_out), T, p,
+                               n_heads, n_kv_heads, head_dim, plan, dtype, int(bool(inverse)),
+                               _stream(stream)), check)
+
+
+def tp_qk_norm_rope(Q, K, wq, wk, positions, Q_out, K_out, T, p, n_heads, n_kv_heads, head_dim,
+                    plan, eps, dtype, stream=None, check=True):
+    """Norm of every query and key head (mean square over the head, weights
+    wq / wk), then the rotation; plan=None: the norm alone."""
+    return _check(_lib.tp_qk_norm_rope(_ptr(Q), _ptr(K), _ptr(wq), _ptr(wk), _ptr(positions),
+                                       _ptr(Q_out), _ptr(K_out), T, p, n_heads, n_kv_heads,
+                                       head_dim, plan, eps, dtype, _stream(stream)), check)
+
+
+def tp_qk_norm_rope_backward(Q, K, wq, wk, positions, dQ_out, dK_out, dQ, dK, dwq, dwk, workspace,
+                             workspace_bytes, T, p, n_heads, n_kv_heads, head_dim, plan, eps,
+                             dtype, stream=None, check=True):
+    """Gradients of tp_qk_norm_rope: dQ, dK and the weights' dwq, dwk."""
+    return _check(_lib.tp_qk_norm_rope_backward(
+        _ptr(Q), _ptr(K), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(dQ_out), _ptr(dK_out), _ptr(dQ),
+        _ptr(dK), _ptr(dwq), _ptr(dwk), _ptr(workspace), workspace_bytes, T, p, n_heads, n_kv_heads,
+        head_dim, plan, eps, dtype, _stream(stream)), check)
+
+
+def tp_qk_norm_rope_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim) -> int:
+    return int(_lib.tp_qk_norm_rope_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim))
 
 
 def tp_debug_exp2_poly(x, y, n, stream=None, check=True):

@@ -504,6 +504,10 @@ tp_status current_device(int* dev, uint64_t* epoch) {
   return device_state(dev, &sms, &cc, &addr, epoch);
 }
 
+tp_status make_launch_ctx(void* stream, bool tensor_core, LaunchCtx* c) {
+  return make_ctx(stream, tensor_core, c);
+}
+
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 void set_error_detail(const char* fmt, ...) {

@@ -25,6 +25,10 @@ struct LaunchCtx {
 // The current device and its context epoch (see LaunchCtx::epoch).
 tp_status current_device(int* dev, uint64_t* epoch);
 
+// Launch context of the current device for `stream`; tensor_core calls need an
+// sm_100 device and take an armed fault injection.
+tp_status make_launch_ctx(void* stream, bool tensor_core, LaunchCtx* c);
+
 // Counts one kernel launch (process-wide, thread-safe).
 void note_launch();
 
@@ -158,6 +162,25 @@ tp_status launch_bwd_dw2(const LaunchCtx& c, const void* Y, const void* dZ, floa
 // ---- attention of every shard's heads (tp_attn_sm100.cu), head_dim 128, bf16
 tp_status launch_tc_attention(const LaunchCtx& c, const void* Q, const void* K, const void* V,
                               void* O, int64_t T, int p, int hq, int hkv, int causal);
+
+// ---- rotary positions and head norms (tp_rope.cu)
+struct RopeCall {
+  const void *Q, *K, *dYq, *dYk;   // dY*: backward only
+  void *Qo, *Ko;
+  const float *wq, *wk;
+  const int32_t* pos;
+  float *dwq, *dwk, *partial;      // backward only
+  const tp_rope_plan* plan;        // null: the norm alone
+  int64_t T;
+  int p, hq, hk, dh, dtype;        // heads per shard (0 where the tensor is null)
+  bool norm, back;                 // back: turn by the negative angle
+  float eps;
+};
+cudaError_t launch_rope(const LaunchCtx& c, const RopeCall& a);
+// Backward of the normed rotation; a.partial holds norm_rope_bwd_ctas(T) rows
+// of 2 * dh sums.
+cudaError_t launch_norm_rope_bwd(const LaunchCtx& c, const RopeCall& a);
+int64_t norm_rope_bwd_ctas(int64_t T);
 
 // ---- the all-reduce of partials held on p GPUs (tp_allreduce.cu)
 // Z_q[rows of the slab] = fixed-order fold of parts[0..p) (+ b2), for q < n_out.

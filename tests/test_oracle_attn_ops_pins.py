@@ -1,0 +1,62 @@
+"""Pins of the oracle's attention-side operators against independent routes
+(closed forms, complex arithmetic, central differences), on the CPU."""
+
+import math
+
+import numpy as np
+import pytest
+
+from oracle import attn_oracle as A
+
+
+def test_rope_frequencies_closed_forms():
+    w = A.rope_frequencies(8, 10000.0)
+    assert np.allclose(w.astype(float), [1.0, 0.1, 0.01, 0.001], rtol=1e-12)
+    assert np.allclose(A.rope_frequencies(8, 10000.0, "linear", 4.0).astype(float), w.astype(float) / 4)
+    # the changed base divides the lowest frequency by the factor and keeps the highest
+    b = A.rope_frequencies(8, 10000.0, "base", 4.0).astype(float)
+    assert b[0] == 1.0 and np.isclose(b[-1], w[-1].astype(float) / 4)
+    # bands: many turns kept, few turns divided, the middle between
+    n = A.rope_frequencies(8, 10000.0, "bands", 8.0, original_len=2 * math.pi * 100, low=1.0,
+                           high=4.0).astype(float)
+    assert n[0] == 1.0 and np.isclose(n[1], 0.1) and np.isclose(n[2], 0.01 / 8) and np.isclose(n[3], 0.001 / 8)
+    n = A.rope_frequencies(8, 10000.0, "bands", 8.0, original_len=2 * math.pi * 250, low=1.0,
+                           high=4.0).astype(float)
+    assert np.isclose(n[2], 0.01 * 0.5 + 0.01 / 8 * 0.5)          # 2.5 turns: half way
+    # ramp over pair indices: index(n) = 8 log(len/2 pi n) / (2 log base)
+    n = A.rope_frequencies(8, 10000.0, "ramp", 4.0, original_len=2 * math.pi * 1000, low=1.0,
+                           high=1000.0).astype(float)
+    assert np.allclose(n, [1.0, 0.1 * (2 / 3 + 1 / 12), 0.01 * (1 / 3 + 2 / 12), 0.001 / 4])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_is_a_complex_product(layout):
+    rng = np.random.default_rng(0)
+    x, pos, w = rng.standard_normal((5, 3, 12)), np.array([0, 1, -7, 1000, 2 ** 31 - 1]), \
+        A.rope_frequencies(8, 100.0)
+    y = A.rope_rotate(x, pos, w, layout, amplitude=1.5)
+    a, b = (x[..., :4], x[..., 4:8]) if layout == "half" else (x[..., 0:8:2], x[..., 1:8:2])
+    z = 1.5 * (a + 1j * b) * np.exp(1j * (pos[:, None].astype(np.longdouble) * w)[:, None, :])
+    ya, yb = (y[..., :4], y[..., 4:8]) if layout == "half" else (y[..., 0:8:2], y[..., 1:8:2])
+    assert np.allclose(ya, z.real, atol=1e-8) and np.allclose(yb, z.imag, atol=1e-8)
+    assert np.array_equal(y[..., 8:], x[..., 8:])
+    back = A.rope_rotate(y, pos, w, layout, amplitude=1 / 1.5, inverse=True)
+    assert np.allclose(back, x, atol=1e-12)
+
+
+def test_head_norm_gradient_against_differences():
+    rng = np.random.default_rng(1)
+    x, w, g, eps = rng.standard_normal((2, 2, 6)), rng.standard_normal(6), rng.standard_normal((2, 2, 6)), 1e-3
+    assert np.allclose((A.head_norm(x, None, 1e-12) ** 2).mean(-1), 1.0)
+    dx, dw = A.head_norm_backward(x, w, g, eps)
+    h = 1e-6
+    for idx in np.ndindex(x.shape):
+        e = np.zeros_like(x)
+        e[idx] = h
+        num = ((A.head_norm(x + e, w, eps) - A.head_norm(x - e, w, eps)) * g).sum() / (2 * h)
+        assert abs(num - dx[idx]) < 1e-8
+    for i in range(6):
+        e = np.zeros(6)
+        e[i] = h
+        num = ((A.head_norm(x, w + e, eps) - A.head_norm(x, w - e, eps)) * g).sum() / (2 * h)
+        assert abs(num - dw[i]) < 1e-8
