@@ -614,6 +614,58 @@ tp_status tp_qk_norm_rope_backward(const void* Q, const void* K, const float* wq
 size_t tp_qk_norm_rope_backward_workspace_size(int64_t T, int p, int n_heads, int n_kv_heads,
                                                int head_dim);
 
+/* Score options of the calls below. */
+typedef struct tp_score_params {
+  float scale;         /* factor on q.k; 0: 1/sqrt(head_dim); else > 0         */
+  float softcap;       /* cap > 0: scores become cap * tanh(score / cap); 0: no */
+  const float* slopes; /* [n_heads] fp32 device, shard by shard, or NULL: the
+                          score of query i and key j gets -slope * |i - j|
+                          after the cap                                        */
+  const void* mask;    /* plan of tp_attention_mask for the call's T, or NULL  */
+  int causal;          /* without a plan: query t sees keys 0..t only          */
+} tp_score_params;
+
+/*
+ * The plan of a mask over T packed tokens: documents behind one another, each
+ * seeing its own tokens only.  Made on the device once a batch, read by every
+ * layer's forward and backward call.
+ *   doc_offsets [n_docs + 1] int32 device: document i is the tokens
+ *               doc_offsets[i] .. doc_offsets[i+1] - 1 (it may be empty); not
+ *               decreasing.  Tokens before the first or behind the last
+ *               document belong to none: as keys nobody sees them, and their
+ *               rows of O, LSE, dQ, dK and dV are left as they were.
+ *   prefix      [n_docs] int32 device or NULL; needs causal: the first
+ *               prefix[i] tokens of document i are seen by all its tokens
+ *               (a longer prefix than the document: all of it)
+ *   causal      nonzero: apart from its prefix a token sees itself and the
+ *               tokens before it
+ *   mask        tp_attention_mask_size(T) bytes, 256-byte aligned: the plan
+ * Offsets outside [0, T] are clamped: no call reads or writes out of range
+ * because of them.
+ */
+tp_status tp_attention_mask(const int32_t* doc_offsets, int n_docs, const int32_t* prefix,
+                            int causal, void* mask, size_t mask_bytes, int64_t T, void* stream);
+
+/* Bytes of a mask plan (0 if T is invalid). */
+size_t tp_attention_mask_size(int64_t T);
+
+/*
+ * Attention of every shard's own heads with scores
+ *   z_ij = cap tanh(scale q_i.k_j / cap) - slope |i - j|
+ * over the keys that row i sees: O_i = sum_j softmax(z_i)_j v_j and
+ * LSE_i = log sum_j exp(z_ij).  Layouts and head rules of tp_attention_heads
+ * (bf16, head_dim 128, query head j on key/value head j / group).
+ *   LSE    [p][n_heads/p][T] fp32 or NULL (the backward call needs it)
+ *   score  NULL: no options (every row sees every key)
+ * A key adds nothing to a row that does not see it, whatever K and V hold
+ * there (infinities and NaN too).  Scores, maxima, sums and the accumulator
+ * are fp32; probabilities are rounded to bf16 before P V and O once at the
+ * end.  The results are reproducible.
+ */
+tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                              int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                              const tp_score_params* score, void* stream);
+
 /* Synchronise `stream`, then report (and clear) the device status word of
  * the current device: TP_ERR_DEVICE_TIMEOUT if a bounded wait ran out since
  * the last call, TP_ERR_CUDA if the stream reported an error, else TP_OK. */

@@ -58,6 +58,9 @@ __all__ = [
     "ROPE_LAYOUT", "ROPE_SCALING", "RopeConfig", "RopePlan", "rope_plan", "tp_rope_plan_init",
     "tp_rope", "tp_qk_norm_rope", "tp_qk_norm_rope_backward",
     "tp_qk_norm_rope_backward_workspace_size",
+    # attention with capped, biased and masked scores
+    "ScoreParams", "score_params", "tp_attention_mask", "tp_attention_mask_size",
+    "tp_attention_scored",
     # the all-reduce of partials held on p GPUs
     "TP_GATHER_MAX", "IpcHandle", "tp_reduce_partials_gather", "tp_ipc_export", "tp_ipc_import",
     "tp_ipc_release",
@@ -129,6 +132,12 @@ class RopePlan(ctypes.Structure):
                 ("turn", ctypes.c_uint64 * 128)]
 
 
+class ScoreParams(ctypes.Structure):
+    """tp_score_params: score options of the scored attention calls."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("causal", ctypes.c_int)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run "
@@ -183,6 +192,11 @@ def _load() -> ctypes.CDLL:
                                                          i32, vp]
     lib.tp_qk_norm_rope_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
     lib.tp_qk_norm_rope_backward_workspace_size.restype = sz
+    score = ctypes.POINTER(ScoreParams)
+    lib.tp_attention_mask.argtypes = [vp, i32, vp, i32, vp, sz, i64, vp]
+    lib.tp_attention_mask_size.argtypes = [i64]
+    lib.tp_attention_mask_size.restype = sz
+    lib.tp_attention_scored.argtypes = [vp] * 5 + [i64, i32, i32, i32, i32, score, vp]
     lib.tp_ipc_export.argtypes = [vp, ctypes.POINTER(IpcHandle)]
     lib.tp_ipc_import.argtypes = [ctypes.POINTER(IpcHandle), ctypes.POINTER(vp)]
     lib.tp_ipc_release.argtypes = [ctypes.POINTER(IpcHandle)]
@@ -199,7 +213,8 @@ def _load() -> ctypes.CDLL:
               "tp_mlp_block_backward_recompute", "tp_sync_status", "tp_abi_version",
               "tp_debug_exp2_poly", "tp_reduce_partials_gather", "tp_ipc_export",
               "tp_ipc_import", "tp_ipc_release", "tp_rope_plan_init", "tp_rope",
-              "tp_qk_norm_rope", "tp_qk_norm_rope_backward"):
+              "tp_qk_norm_rope", "tp_qk_norm_rope_backward", "tp_attention_mask",
+              "tp_attention_scored"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -457,6 +472,34 @@ def tp_qk_norm_rope_backward(Q, K, wq, wk, positions, dQ_out, dK_out, dQ, dK, dw
 
 def tp_qk_norm_rope_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim) -> int:
     return int(_lib.tp_qk_norm_rope_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim))
+
+
+def score_params(scale=0.0, softcap=0.0, slopes=None, mask=None, causal=False) -> ScoreParams:
+    """Score options (tp_score_params); the buffers stay referenced by the result."""
+    prm = ScoreParams(scale, softcap, _ptr(slopes), _ptr(mask), int(bool(causal)))
+    prm.buffers = (slopes, mask)
+    return prm
+
+
+def tp_attention_mask(doc_offsets, n_docs, prefix, causal, mask, mask_bytes, T, stream=None,
+                      check=True):
+    """The plan of a document / prefix mask over T packed tokens, into `mask`."""
+    return _check(_lib.tp_attention_mask(_ptr(doc_offsets), n_docs, _ptr(prefix),
+                                         int(bool(causal)), _ptr(mask), mask_bytes, T,
+                                         _stream(stream)), check)
+
+
+def tp_attention_mask_size(T) -> int:
+    return int(_lib.tp_attention_mask_size(T))
+
+
+def tp_attention_scored(Q, K, V, O, LSE, T, p, n_heads, n_kv_heads, head_dim, score=None,
+                        stream=None, check=True):
+    """Attention of every shard's own heads with capped, biased and masked
+    scores (score_params); LSE (or None) gets log sum exp of every row."""
+    return _check(_lib.tp_attention_scored(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), T, p,
+                                           n_heads, n_kv_heads, head_dim, score, _stream(stream)),
+                  check)
 
 
 def tp_debug_exp2_poly(x, y, n, stream=None, check=True):

@@ -11,6 +11,7 @@
 
 #include "tp_internal.h"
 #include "tp_launch.cuh"
+#include "tp_score.h"
 #include "tp_mlp.h"
 
 namespace tpk {
@@ -138,6 +139,49 @@ tp_status rope_impl(RopeCall a, int n_heads, int n_kv_heads, void* stream) {
 
 size_t norm_rope_ws(int64_t T, int dh) {
   return align256(static_cast<size_t>(norm_rope_bwd_ctas(T)) * 2 * dh * 4);
+}
+
+// Heads and options of a scored-attention call into `a`.
+tp_status score_call(ScoreCall* a, int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                     const tp_score_params* s) {
+  TP_TRY(check_layout(T, p, n_heads, n_kv_heads, head_dim, true, true));
+  if (n_heads % n_kv_heads != 0)
+    TP_FAIL(TP_ERR_INVALID_ARG, "n_heads (%d) must be a multiple of n_kv_heads (%d)", n_heads,
+            n_kv_heads);
+  if (head_dim != 128) TP_FAIL(TP_ERR_UNSUPPORTED, "head_dim %d (128 is provided)", head_dim);
+  // unit counts and TMA coordinates stay in int32
+  if (T > (int64_t(1) << 30) ||
+      static_cast<int64_t>(n_heads) * (T / kAttnTile + 2) > (int64_t(1) << 30))
+    TP_FAIL(TP_ERR_UNSUPPORTED, "sizes too large (T = %lld, %d heads)", (long long)T, n_heads);
+  a->T = T;
+  a->p = p;
+  a->hq = n_heads / p;
+  a->hkv = n_kv_heads / p;
+  a->scale = 1.0f / std::sqrt(static_cast<float>(head_dim));
+  if (s == nullptr) return TP_OK;
+  if (s->scale != 0.0f) {
+    if (!(s->scale > 0.0f) || !std::isfinite(s->scale))
+      TP_FAIL(TP_ERR_INVALID_ARG, "scale must be > 0 (or 0 for 1/sqrt(head_dim))");
+    a->scale = s->scale;
+  }
+  if (!(s->softcap >= 0.0f) || !std::isfinite(s->softcap))
+    TP_FAIL(TP_ERR_INVALID_ARG, "softcap must be >= 0");
+  if (s->softcap > 0.0f && (s->softcap < 1e-3f || s->softcap > 1e6f ||
+                            a->scale / s->softcap < 1e-9f || a->scale / s->softcap > 1e6f))
+    TP_FAIL(TP_ERR_UNSUPPORTED, "softcap 1e-3 to 1e6 and scale/softcap 1e-9 to 1e6 are provided");
+  if (!aligned(s->slopes, 4)) TP_FAIL(TP_ERR_ALIGNMENT, "slopes must be 4-byte aligned");
+  if (!aligned(s->mask, 256)) TP_FAIL(TP_ERR_ALIGNMENT, "mask must be 256-byte aligned");
+  a->cap = s->softcap;
+  a->slopes = s->slopes;
+  a->mask = s->mask;
+  a->causal = s->causal != 0;
+  return TP_OK;
+}
+
+tp_status check_bf16(const void* p, const char* name) {
+  if (p == nullptr) TP_FAIL(TP_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(p, 16)) TP_FAIL(TP_ERR_ALIGNMENT, "%s must be 16-byte aligned", name);
+  return TP_OK;
 }
 
 }  // namespace
@@ -310,6 +354,66 @@ tp_status tp_qk_norm_rope_backward(const void* Q, const void* K, const float* wq
   LaunchCtx c{};
   TP_TRY(make_launch_ctx(stream, false, &c));
   return cuda_status(launch_norm_rope_bwd(c, a), "head norm backward launch");
+}
+
+size_t tp_attention_mask_size(int64_t T) {
+  return T < 0 || T > (int64_t(1) << 30) ? 0 : T == 0 ? 256 : mask_bytes(T);
+}
+
+tp_status tp_attention_mask(const int32_t* doc_offsets, int n_docs, const int32_t* prefix,
+                            int causal, void* mask, size_t mask_size, int64_t T, void* stream) {
+  set_error_detail("%s", "");
+  if (T < 0) TP_FAIL(TP_ERR_INVALID_ARG, "T = %lld", (long long)T);
+  if (T > (int64_t(1) << 30)) TP_FAIL(TP_ERR_UNSUPPORTED, "T = %lld", (long long)T);
+  if (n_docs < 1 || n_docs > (1 << 30)) TP_FAIL(TP_ERR_INVALID_ARG, "n_docs = %d", n_docs);
+  if (prefix != nullptr && !causal)
+    TP_FAIL(TP_ERR_INVALID_ARG, "a prefix needs causal: without it every token of a document is seen");
+  if (T == 0) return TP_OK;
+  if (doc_offsets == nullptr) TP_FAIL(TP_ERR_INVALID_ARG, "doc_offsets is NULL");
+  if (!aligned(doc_offsets, 4) || !aligned(prefix, 4))
+    TP_FAIL(TP_ERR_ALIGNMENT, "doc_offsets and prefix must be 4-byte aligned");
+  if (mask == nullptr || mask_size < mask_bytes(T))
+    TP_FAIL(TP_ERR_WORKSPACE, "the mask plan needs %zu bytes, got %zu", mask_bytes(T),
+            mask == nullptr ? size_t(0) : mask_size);
+  if (!aligned(mask, 256)) TP_FAIL(TP_ERR_ALIGNMENT, "mask must be 256-byte aligned");
+  const size_t n = static_cast<size_t>(n_docs) * 4;
+  TP_TRY(check_overlaps({{"mask", mask, mask_bytes(T), nullptr}},
+                        {{"doc_offsets", doc_offsets, n + 4, nullptr},
+                         {"prefix", prefix, n, nullptr}}));
+  LaunchCtx c{};
+  TP_TRY(make_launch_ctx(stream, false, &c));
+  return cuda_status(launch_attention_mask(c, doc_offsets, n_docs, prefix, causal != 0, mask, T),
+                     "mask launch");
+}
+
+tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                              int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                              const tp_score_params* score, void* stream) {
+  set_error_detail("%s", "");
+  ScoreCall a{};
+  TP_TRY(score_call(&a, T, p, n_heads, n_kv_heads, head_dim, score));
+  if (T == 0) return TP_OK;
+  TP_TRY(check_bf16(Q, "Q"));
+  TP_TRY(check_bf16(K, "K"));
+  TP_TRY(check_bf16(V, "V"));
+  TP_TRY(check_bf16(O, "O"));
+  if (!aligned(LSE, 4)) TP_FAIL(TP_ERR_ALIGNMENT, "LSE must be 4-byte aligned");
+  const size_t t = static_cast<size_t>(T), q = t * n_heads * 256, kv = t * n_kv_heads * 256;
+  const size_t lse = t * n_heads * 4;
+  TP_TRY(check_overlaps({{"O", O, q, nullptr}, {"LSE", LSE, lse, nullptr}},
+                        {{"Q", Q, q, nullptr},
+                         {"K", K, kv, nullptr},
+                         {"V", V, kv, nullptr},
+                         {"slopes", a.slopes, static_cast<size_t>(n_heads) * 4, nullptr},
+                         {"mask", a.mask, mask_bytes(T), nullptr}}));
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.O = O;
+  a.LSE = LSE;
+  LaunchCtx c{};
+  TP_TRY(make_launch_ctx(stream, true, &c));
+  return launch_attention_scored(c, a);
 }
 
 }  // extern "C"

@@ -52,6 +52,7 @@
 #include "tp_device.cuh"
 #include "tp_internal.h"
 #include "tp_launch.cuh"
+#include "tp_softmax.cuh"
 
 namespace tpk {
 namespace {
@@ -68,10 +69,9 @@ constexpr int NUM_THREADS = 384;
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BQ, BKV, /*a_mn=*/0, /*b_mn=*/0);  // Q K^T
 constexpr uint32_t IDESC_O = idesc_bf16_f32(BQ, DH, /*a_mn=*/0, /*b_mn=*/1);   // P V
 constexpr uint32_t O_COL0 = NQT * BKV, TMEM_COLS = 512;   // S_t at t*128, O_t at 256 + t*128
-constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float RESCALE_LOG2 = 8.0f;    // move the running maximum only past this growth
 constexpr int POLY_PAIRS = 2;           // of every 8 probability pairs, this many use the
-                                        // polynomial exp2 on the FMA pipe, the rest MUFU    // move the running maximum only past this growth
-constexpr unsigned kErrWaitAttn = 1u << 6;
+                                        // polynomial exp2 on the FMA pipe, the rest MUFU
 
 struct AttnParams {
   int32_t T, p, hq, hkv, group, q_blocks, q_pairs, num_units, causal;
@@ -115,56 +115,6 @@ __device__ __forceinline__ Unit decode_unit(const AttnParams& P, int32_t u) {
 __device__ __forceinline__ int32_t unit_of(int32_t r) {
   const int32_t g = static_cast<int32_t>(gridDim.x), b = static_cast<int32_t>(blockIdx.x);
   return r * g + ((r & 1) ? g - 1 - b : b);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  uint32_t u;
-  memcpy(&u, &v, 4);
-  return u;
-}
-
-// The softmax's hot loop uses the packed fp32 pair helpers f2_* of
-// tp_device.cuh (sm_100 FFMA2 / FADD2: two lanes per instruction).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// 2^x on the FMA pipe, for part of the probabilities so that the MUFU unit
-// (16 exp2 per clock per SM) is not the only one computing them: range
-// reduction to the nearest integer n (x = n + f, |f| <= 1/2, by the
-// 1.5 * 2^23 rounding constant), a degree-4 polynomial for 2^f whose
-// coefficients were fitted to minimise the relative error on [-1/2, 1/2]
-// (iteratively reweighted least squares; max relative error of the fit
-// 2.6e-6, of the fp32 evaluation below at most 2.7e-6 on [-126, 0]), and n
-// added to the exponent field.  x is clamped to >= -126 (the probabilities
-// are bf16, so 2^-126 and 0 are the same to them).  Two lanes per call.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
-  float x0, x1;
-  f2_unpack(x2, x0, x1);
-  x2 = f2_pack(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
-  const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);
-  const uint64_t t = f2_add(x2, magic);
-  const uint64_t n = f2_add(t, f2_pack(-12582912.0f, -12582912.0f));
-  const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x2);
-  uint64_t p = f2_fma(f2_pack(0.009570101276040077f, 0.009570101276040077f), f,
-                      f2_pack(0.05591785907745361f, 0.05591785907745361f));
-  p = f2_fma(p, f, f2_pack(0.240247443318367f, 0.240247443318367f));
-  p = f2_fma(p, f, f2_pack(0.6931217908859253f, 0.6931217908859253f));
-  p = f2_fma(p, f, f2_pack(0.9999992847442627f, 0.9999992847442627f));
-  float p0, p1, t0, t1;
-  f2_unpack(p, p0, p1);
-  f2_unpack(t, t0, t1);
-  return f2_pack(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
-                 __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23)));
 }
 
 // One softmax step of a thread's row over a 128-key block in TMEM columns

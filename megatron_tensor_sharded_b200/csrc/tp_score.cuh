@@ -1,0 +1,151 @@
+// Device parts of scored attention: which keys a row and a tile see, the
+// scores' cap and bias, and the look at operand rows that are not finite.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "tp_device.cuh"
+#include "tp_score.h"
+#include "tp_softmax.cuh"
+
+namespace tpk {
+
+// Key blocks [jb, je) that a tile of 128 query rows visits; block j is whole
+// when every row of the tile sees all of it.
+struct TileSpan {
+  int32_t jb, je, in_lo, in_hi;
+  __device__ __forceinline__ bool whole(int32_t j) const {
+    return j * kAttnTile >= in_lo && (j + 1) * kAttnTile <= in_hi;
+  }
+};
+
+__device__ __forceinline__ TileSpan tile_span(const MaskPlan& m, int32_t qb, int32_t q_blocks,
+                                              int32_t T, int32_t causal) {
+  TileSpan s{0, 0, 0, 0};
+  if (qb >= q_blocks) return s;
+  if (m.rows != nullptr) {
+    const int4 t = m.q_tiles[qb];
+    if (t.x >= t.y) return s;
+    s.jb = t.x / kAttnTile;
+    s.je = (t.y + kAttnTile - 1) / kAttnTile;
+    s.in_lo = t.z;
+    s.in_hi = t.w;
+    return s;
+  }
+  const int32_t hi = causal ? min((qb + 1) * kAttnTile, T) : T;
+  s.je = (hi + kAttnTile - 1) / kAttnTile;
+  s.in_hi = causal ? qb * kAttnTile + 1 : T;
+  return s;
+}
+
+// Keys [x, y) that query row q sees; y < 0: the row lies in no document.
+__device__ __forceinline__ int2 row_span(const MaskPlan& m, int32_t q, int32_t T, int32_t causal) {
+  if (m.rows != nullptr) return q < T ? m.rows[q] : make_int2(0, -1);
+  return make_int2(0, causal ? min(q + 1, T) : T);
+}
+
+// 32 raw products -> capped scores in log2 units.  True where the warp took
+// the MUFU form (some row's |scale s| > cap/2, or a NaN).
+__device__ __forceinline__ bool cap_chunk(uint32_t* v, const ScoreConsts& S) {
+  float mx[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    mx[0] = max3_nan(mx[0], fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
+    mx[1] = max3_nan(mx[1], fabsf(__uint_as_float(v[e + 2])), fabsf(__uint_as_float(v[e + 3])));
+  }
+  const bool slow = !__all_sync(0xffffffffu, max3_nan(mx[0], mx[1], mx[1]) <= S.small);
+  if (!slow) {
+    const uint64_t c0 = f2_pack(S.poly[0], S.poly[0]), c1 = f2_pack(S.poly[1], S.poly[1]);
+    const uint64_t c2 = f2_pack(S.poly[2], S.poly[2]), c3 = f2_pack(S.poly[3], S.poly[3]);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t s = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+      const uint64_t u = f2_mul(s, s);
+      const uint64_t z = f2_mul(s, f2_fma(u, f2_fma(u, f2_fma(u, c3, c2), c1), c0));
+      float a, b;
+      f2_unpack(z, a, b);
+      v[e] = __float_as_uint(a);
+      v[e + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float s = __uint_as_float(v[e]);
+      const float t = 1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s) * S.two_x));
+      v[e] = __float_as_uint(S.cap_log2 * copysignf(t, s));
+    }
+  }
+  return slow;
+}
+
+// Scores -> scores - slope2 |dist0 + e|, all in log2 units; SCALE: v holds raw
+// products and is scaled too.  side: -1 every key is at or before every row of
+// the tile, 1 at or behind it (the distance is then linear in e), 0 mixed.
+template <bool SCALE>
+__device__ __forceinline__ void bias_chunk(uint32_t* v, float scale, float slope2, float dist0,
+                                           int side) {
+  if (side != 0) {
+    const float g = side < 0 ? slope2 : -slope2;
+    const uint64_t g2 = f2_pack(g, g), sc = f2_pack(scale, scale);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t d = f2_pack(dist0 + static_cast<float>(e), dist0 + static_cast<float>(e + 1));
+      const uint64_t s = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+      const uint64_t z = SCALE ? f2_fma(s, sc, f2_mul(d, g2)) : f2_fma(d, g2, s);
+      float a, b;
+      f2_unpack(z, a, b);
+      v[e] = __float_as_uint(a);
+      v[e + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float s = SCALE ? __uint_as_float(v[e]) * scale : __uint_as_float(v[e]);
+      v[e] = __float_as_uint(fmaf(-slope2, fabsf(dist0 + static_cast<float>(e)), s));
+    }
+  }
+}
+
+// Columns outside [rl, rh) of a 32-column chunk become -inf.
+__device__ __forceinline__ void mask_chunk(uint32_t* v, int32_t rl, int32_t rh) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (e < rl || e >= rh) v[e] = 0xff800000u;
+}
+
+// Whether row `row` (0..127) of a 128 x 128 bf16 tile in shared memory (two
+// 64-column halves, 128-byte swizzle) holds an infinity or a NaN; zeroing it.
+__device__ __forceinline__ uint32_t row_chunk_addr(uint32_t tile, int row, int c) {
+  return tile + (c >> 3) * 16384u + row * 128u + (((c & 7) ^ (row & 7)) * 16u);
+}
+__device__ __forceinline__ bool row_not_finite(uint32_t tile, int row) {
+  // x * 0 + a is NaN from the first infinity or NaN on
+  __nv_bfloat162 a = __floats2bfloat162_rn(0.0f, 0.0f);
+  const __nv_bfloat162 zero = a;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(row_chunk_addr(tile, row, c)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 x;
+      memcpy(&x, &w[i], 4);
+      a = __hfma2(x, zero, a);
+    }
+  }
+  return __hisnan(__low2bfloat16(a)) || __hisnan(__high2bfloat16(a));
+}
+__device__ __forceinline__ void zero_row(uint32_t tile, int row) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row_chunk_addr(tile, row, c)),
+                 "r"(0)
+                 : "memory");
+}
+
+}  // namespace tpk

@@ -1,0 +1,91 @@
+// Scored attention: what the kernels share with the launchers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "tp_internal.h"
+
+namespace tpk {
+
+constexpr int kAttnTile = 128;   // query rows and key rows of a tile
+
+// The mask's plan (tp_attention_mask): per query row the keys it sees, [x, y)
+// (y < 0: the row lies in no document); per tile of 128 query rows {least x,
+// greatest y, greatest x, least y}, the first two over rows in a document; per
+// tile of 128 keys the query tiles [x, y) that may see one of them.
+struct MaskPlan {
+  int2* rows;
+  int4* q_tiles;
+  int2* k_tiles;
+};
+inline size_t mask_align(size_t n) { return (n + 255) & ~size_t(255); }
+inline MaskPlan mask_plan(const void* buf, int64_t T) {
+  if (buf == nullptr) return MaskPlan{};
+  const size_t tiles = static_cast<size_t>(ceil_div(T, kAttnTile));
+  uint8_t* b = static_cast<uint8_t*>(const_cast<void*>(buf));
+  const size_t r = mask_align(static_cast<size_t>(T) * sizeof(int2));
+  return MaskPlan{reinterpret_cast<int2*>(b), reinterpret_cast<int4*>(b + r),
+                  reinterpret_cast<int2*>(b + r + mask_align(tiles * sizeof(int4)))};
+}
+inline size_t mask_bytes(int64_t T) {
+  const size_t tiles = static_cast<size_t>(ceil_div(T, kAttnTile));
+  return mask_align(static_cast<size_t>(T) * sizeof(int2)) + mask_align(tiles * sizeof(int4)) +
+         mask_align(tiles * sizeof(int2));
+}
+
+// Scores z of a raw product s = q.k, in units of log2: z = log2(e) *
+// (cap tanh(scale s / cap) - slope |i - j|).
+struct ScoreConsts {
+  float scale_log2;    // log2(e) scale
+  float poly[4];       // z = s (p0 + u (p1 + u (p2 + u p3))), u = s^2, for |s| <= small
+  float small;         // scale |s| / cap <= 1/2
+  float two_x;         // 2 log2(e) scale / cap: tanh by e^(2x) beyond it
+  float cap_log2;      // log2(e) cap (0: scores are not capped)
+  float scale;         // scale itself (gradients)
+  float x_of_s;        // scale / cap
+};
+inline ScoreConsts score_consts(float scale, float cap) {
+  const double l2e = 1.4426950408889634;
+  // tanh(x)/x in u = x^2 on [0, 1/4]: least-squares fit reweighted to the
+  // smallest relative error, 5.5e-7
+  const double c[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993,
+                       -0.04440222680568695};
+  ScoreConsts k{};
+  k.scale = scale;
+  k.scale_log2 = static_cast<float>(l2e * scale);
+  if (cap > 0.0f) {
+    const double x = static_cast<double>(scale) / cap;
+    for (int i = 0; i < 4; ++i) k.poly[i] = static_cast<float>(l2e * cap * c[i] * std::pow(x, 2 * i + 1));
+    k.small = static_cast<float>(0.5 / x);
+    k.two_x = static_cast<float>(2.0 * l2e * x);
+    k.cap_log2 = static_cast<float>(l2e * cap);
+    k.x_of_s = static_cast<float>(x);
+  }
+  return k;
+}
+
+struct ScoreCall {
+  const void *Q, *K, *V;
+  void* O;
+  float* LSE;              // forward: may be null
+  const void* dO;          // backward
+  void *dQ, *dK, *dV;
+  float* delta;            // backward: [p][hq][T] scratch
+  int64_t T;
+  int p, hq, hkv;          // heads per shard
+  bool causal;
+  float scale, cap;
+  const float* slopes;     // [p*hq] or null
+  const void* mask;        // plan or null
+};
+
+cudaError_t launch_attention_mask(const LaunchCtx& c, const int32_t* off, int n_docs,
+                                  const int32_t* prefix, bool causal, void* mask, int64_t T);
+tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a);
+tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a);
+
+}  // namespace tpk

@@ -72,3 +72,57 @@ def head_norm_backward(x, w, g, eps):
     dw = (g * xhat).sum((0, 1))
     gw = g * (1.0 if w is None else w)
     return (gw - xhat * (gw * xhat).mean(-1, keepdims=True)) / rms, dw
+
+
+# ------------------------------------------------------- scored attention
+def visible(T, causal, doc_offsets=None, prefix=None):
+    """([T, T] bool: row i sees key j, [T] bool: row i lies in a document)."""
+    seen, inside = np.zeros((T, T), bool), np.zeros(T, bool)
+    offs = [0, T] if doc_offsets is None else list(doc_offsets)
+    for d, (a, b) in enumerate(zip(offs, offs[1:])):
+        a, b = max(a, 0), min(b, T)
+        for i in range(a, b):
+            inside[i] = True
+            seen[i, a:(i + 1 if causal else b)] = True
+            if causal and prefix is not None:
+                seen[i, a:min(b, a + max(prefix[d], 0))] = True
+    return seen, inside
+
+
+def scores(q, k, scale, cap=0.0, slope=0.0):
+    """(z [Tq, Tk], tanh or None) of one head; distances |i - j|."""
+    z = scale * (np.asarray(q, np.float64) @ np.asarray(k, np.float64).T)
+    t = None
+    if cap:
+        t = np.tanh(z / cap)
+        z = cap * t
+    i, j = np.arange(z.shape[0]), np.arange(z.shape[1])
+    return z - slope * np.abs(i[:, None] - j[None, :]), t
+
+
+def scored_head(q, k, v, seen, scale, cap=0.0, slope=0.0):
+    """(O, LSE) of one head over the keys that each row sees; rows that see
+    nothing give 0 and -inf."""
+    z, _ = scores(q, k, scale, cap, slope)
+    z = np.where(seen, z, -np.inf)
+    m = z.max(1, keepdims=True)
+    m = np.where(np.isfinite(m), m, 0.0)
+    e = np.exp(z - m)
+    l = e.sum(1, keepdims=True)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        o = np.where(l > 0, (e @ np.asarray(v, np.float64)) / l, 0.0)
+        return o, (m + np.log(l))[:, 0]
+
+
+def scored_head_backward(q, k, v, do, seen, scale, cap=0.0, slope=0.0):
+    """(dq, dk, dv) of one head for the upstream gradient do."""
+    q, k, v, do = (np.asarray(x, np.float64) for x in (q, k, v, do))
+    z, t = scores(q, k, scale, cap, slope)
+    _, lse = scored_head(q, k, v, seen, scale, cap, slope)
+    P = np.where(seen, np.exp(np.where(seen, z, 0.0) - np.where(np.isfinite(lse), lse, 0.0)[:, None]), 0.0)
+    dP = do @ v.T
+    dz = P * (dP - (P * dP).sum(1, keepdims=True))
+    if t is not None:
+        dz = dz * (1 - t * t)
+    dz = dz * scale
+    return dz @ k, dz.T @ q, P.T @ do

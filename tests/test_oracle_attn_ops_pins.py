@@ -60,3 +60,49 @@ def test_head_norm_gradient_against_differences():
         e[i] = h
         num = ((A.head_norm(x, w + e, eps) - A.head_norm(x, w - e, eps)) * g).sum() / (2 * h)
         assert abs(num - dw[i]) < 1e-8
+
+
+def test_visible_by_hand():
+    s, inside = A.visible(6, True, [0, 2, 2, 5], [0, 9, 2])
+    want = np.array([[1, 0, 0, 0, 0, 0], [1, 1, 0, 0, 0, 0], [0, 0, 1, 1, 0, 0], [0, 0, 1, 1, 0, 0],
+                     [0, 0, 1, 1, 1, 0], [0, 0, 0, 0, 0, 0]], bool)
+    assert np.array_equal(s, want) and list(inside) == [1, 1, 1, 1, 1, 0]
+    assert A.visible(3, False)[0].all()
+
+
+def test_scored_head_against_torch_and_closed_forms():
+    torch = pytest.importorskip("torch")
+    rng = np.random.default_rng(2)
+    q, k, v = (rng.standard_normal((9, 4)) for _ in range(3))
+    seen, _ = A.visible(9, True)
+    o, lse = A.scored_head(q, k, v, seen, 0.5)
+    tt = [torch.from_numpy(x)[None, None] for x in (q, k, v)]
+    want = torch.nn.functional.scaled_dot_product_attention(*tt, is_causal=True, scale=0.5)[0, 0].numpy()
+    assert np.allclose(o, want, atol=1e-12)
+    assert np.isclose(lse[0], 0.5 * q[0] @ k[0])
+    # a large cap changes nothing, a tiny one makes all keys alike
+    assert np.allclose(A.scored_head(q, k, v, seen, 0.5, cap=1e7)[0], o, atol=1e-9)
+    flat = A.scored_head(q, k, v, np.ones((9, 9), bool), 0.5, cap=1e-9)[0]
+    assert np.allclose(flat, v.mean(0))
+    # a huge slope leaves the row itself
+    assert np.allclose(A.scored_head(q, k, v, np.ones((9, 9), bool), 0.5, slope=1e4)[0], v)
+    o, lse = A.scored_head(q, k, v, np.zeros((9, 9), bool), 0.5)
+    assert not o.any() and np.all(lse == -np.inf)
+
+
+@pytest.mark.parametrize("cap,slope", [(0.0, 0.0), (1.5, 0.0), (0.0, 0.3), (0.8, -0.2)])
+def test_scored_gradients_against_differences(cap, slope):
+    rng = np.random.default_rng(3)
+    x = [rng.standard_normal((6, 3)) for _ in range(3)]
+    do = rng.standard_normal((6, 3))
+    seen, _ = A.visible(6, True, [0, 4, 5], [2, 0])
+    grads = A.scored_head_backward(*x, do, seen, 0.7, cap, slope)
+    h = 1e-6
+    for n in range(3):
+        for idx in np.ndindex(6, 3):
+            y = [a.copy() for a in x]
+            y[n][idx] += h
+            up = (A.scored_head(*y, seen, 0.7, cap, slope)[0] * do).sum()
+            y[n][idx] -= 2 * h
+            down = (A.scored_head(*y, seen, 0.7, cap, slope)[0] * do).sum()
+            assert abs((up - down) / (2 * h) - grads[n][idx]) < 1e-7
