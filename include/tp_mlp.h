@@ -666,6 +666,31 @@ tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void*
                               int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
                               const tp_score_params* score, void* stream);
 
+/*
+ * Its backward: dQ, dK, dV for the upstream gradient dO.
+ *   P = exp(z - LSE), D_i = sum_d dO_id O_id, t = tanh(scale q.k / cap):
+ *   dV_j = sum_i P_ij dO_i,  dS_ij = P_ij (dO_i.v_j - D_i) (1 - t_ij^2),
+ *   dQ_i = scale sum_j dS_ij k_j,  dK_j = scale sum_i dS_ij q_i,
+ * dK and dV summed over the query heads of a group.  The slopes get no
+ * gradient.
+ *   Q, K, V, O, LSE, score  of the forward call;  dO as O
+ *   dQ as Q, dK as K, dV as V (bf16 outputs); the rows of tokens in no
+ *          document are left as they were
+ *   workspace  tp_attention_scored_backward_workspace_size(...) bytes,
+ *              256-byte aligned
+ * P and dS are rounded to bf16 before their products, the gradients once at
+ * the end; sums are fp32 in a fixed order (reproducible).
+ */
+tp_status tp_attention_scored_backward(const void* Q, const void* K, const void* V, const void* O,
+                                       const float* LSE, const void* dO, void* dQ, void* dK,
+                                       void* dV, void* workspace, size_t workspace_bytes,
+                                       int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                                       const tp_score_params* score, void* stream);
+
+/* Workspace bytes tp_attention_scored_backward needs (0 if the arguments are invalid). */
+size_t tp_attention_scored_backward_workspace_size(int64_t T, int p, int n_heads, int n_kv_heads,
+                                                   int head_dim);
+
 /* Synchronise `stream`, then report (and clear) the device status word of
  * the current device: TP_ERR_DEVICE_TIMEOUT if a bounded wait ran out since
  * the last call, TP_ERR_CUDA if the stream reported an error, else TP_OK. */

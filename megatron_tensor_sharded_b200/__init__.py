@@ -60,7 +60,8 @@ __all__ = [
     "tp_qk_norm_rope_backward_workspace_size",
     # attention with capped, biased and masked scores
     "ScoreParams", "score_params", "tp_attention_mask", "tp_attention_mask_size",
-    "tp_attention_scored",
+    "tp_attention_scored", "tp_attention_scored_backward",
+    "tp_attention_scored_backward_workspace_size",
     # the all-reduce of partials held on p GPUs
     "TP_GATHER_MAX", "IpcHandle", "tp_reduce_partials_gather", "tp_ipc_export", "tp_ipc_import",
     "tp_ipc_release",
@@ -197,6 +198,9 @@ def _load() -> ctypes.CDLL:
     lib.tp_attention_mask_size.argtypes = [i64]
     lib.tp_attention_mask_size.restype = sz
     lib.tp_attention_scored.argtypes = [vp] * 5 + [i64, i32, i32, i32, i32, score, vp]
+    lib.tp_attention_scored_backward.argtypes = [vp] * 10 + [sz, i64, i32, i32, i32, i32, score, vp]
+    lib.tp_attention_scored_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    lib.tp_attention_scored_backward_workspace_size.restype = sz
     lib.tp_ipc_export.argtypes = [vp, ctypes.POINTER(IpcHandle)]
     lib.tp_ipc_import.argtypes = [ctypes.POINTER(IpcHandle), ctypes.POINTER(vp)]
     lib.tp_ipc_release.argtypes = [ctypes.POINTER(IpcHandle)]
@@ -214,7 +218,7 @@ def _load() -> ctypes.CDLL:
               "tp_debug_exp2_poly", "tp_reduce_partials_gather", "tp_ipc_export",
               "tp_ipc_import", "tp_ipc_release", "tp_rope_plan_init", "tp_rope",
               "tp_qk_norm_rope", "tp_qk_norm_rope_backward", "tp_attention_mask",
-              "tp_attention_scored"):
+              "tp_attention_scored", "tp_attention_scored_backward"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -500,6 +504,20 @@ def tp_attention_scored(Q, K, V, O, LSE, T, p, n_heads, n_kv_heads, head_dim, sc
     return _check(_lib.tp_attention_scored(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), T, p,
                                            n_heads, n_kv_heads, head_dim, score, _stream(stream)),
                   check)
+
+
+def tp_attention_scored_backward(Q, K, V, O, LSE, dO, dQ, dK, dV, workspace, workspace_bytes, T, p,
+                                 n_heads, n_kv_heads, head_dim, score=None, stream=None,
+                                 check=True):
+    """Gradients of tp_attention_scored: dQ, dK, dV."""
+    return _check(_lib.tp_attention_scored_backward(
+        _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV),
+        _ptr(workspace), workspace_bytes, T, p, n_heads, n_kv_heads, head_dim, score,
+        _stream(stream)), check)
+
+
+def tp_attention_scored_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim) -> int:
+    return int(_lib.tp_attention_scored_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim))
 
 
 def tp_debug_exp2_poly(x, y, n, stream=None, check=True):

@@ -178,6 +178,11 @@ tp_status score_call(ScoreCall* a, int64_t T, int p, int n_heads, int n_kv_heads
   return TP_OK;
 }
 
+// Backward workspace: D, one number a query row and head.
+size_t score_bwd_ws(const ScoreCall& a) {
+  return align256(static_cast<size_t>(a.T) * a.p * a.hq * 4);
+}
+
 tp_status check_bf16(const void* p, const char* name) {
   if (p == nullptr) TP_FAIL(TP_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned(p, 16)) TP_FAIL(TP_ERR_ALIGNMENT, "%s must be 16-byte aligned", name);
@@ -414,6 +419,62 @@ tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void*
   LaunchCtx c{};
   TP_TRY(make_launch_ctx(stream, true, &c));
   return launch_attention_scored(c, a);
+}
+
+size_t tp_attention_scored_backward_workspace_size(int64_t T, int p, int n_heads, int n_kv_heads,
+                                                   int head_dim) {
+  ScoreCall a{};
+  if (score_call(&a, T, p, n_heads, n_kv_heads, head_dim, nullptr) != TP_OK) return 0;
+  return T == 0 ? 256 : score_bwd_ws(a);
+}
+
+tp_status tp_attention_scored_backward(const void* Q, const void* K, const void* V, const void* O,
+                                       const float* LSE, const void* dO, void* dQ, void* dK,
+                                       void* dV, void* workspace, size_t workspace_bytes,
+                                       int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                                       const tp_score_params* score, void* stream) {
+  set_error_detail("%s", "");
+  ScoreCall a{};
+  TP_TRY(score_call(&a, T, p, n_heads, n_kv_heads, head_dim, score));
+  if (T == 0) return TP_OK;
+  TP_TRY(check_bf16(Q, "Q"));
+  TP_TRY(check_bf16(K, "K"));
+  TP_TRY(check_bf16(V, "V"));
+  TP_TRY(check_bf16(O, "O"));
+  TP_TRY(check_bf16(dO, "dO"));
+  TP_TRY(check_bf16(dQ, "dQ"));
+  TP_TRY(check_bf16(dK, "dK"));
+  TP_TRY(check_bf16(dV, "dV"));
+  if (LSE == nullptr) TP_FAIL(TP_ERR_INVALID_ARG, "LSE is NULL");
+  if (!aligned(LSE, 4)) TP_FAIL(TP_ERR_ALIGNMENT, "LSE must be 4-byte aligned");
+  const size_t need = score_bwd_ws(a);
+  TP_TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t t = static_cast<size_t>(T), q = t * n_heads * 256, kv = t * n_kv_heads * 256;
+  TP_TRY(check_overlaps({{"dQ", dQ, q, nullptr},
+                         {"dK", dK, kv, nullptr},
+                         {"dV", dV, kv, nullptr},
+                         {"workspace", workspace, need, nullptr}},
+                        {{"Q", Q, q, nullptr},
+                         {"K", K, kv, nullptr},
+                         {"V", V, kv, nullptr},
+                         {"O", O, q, nullptr},
+                         {"dO", dO, q, nullptr},
+                         {"LSE", LSE, t * n_heads * 4, nullptr},
+                         {"slopes", a.slopes, static_cast<size_t>(n_heads) * 4, nullptr},
+                         {"mask", a.mask, mask_bytes(T), nullptr}}));
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.O = const_cast<void*>(O);
+  a.LSE = const_cast<float*>(LSE);
+  a.dO = dO;
+  a.dQ = dQ;
+  a.dK = dK;
+  a.dV = dV;
+  a.delta = static_cast<float*>(workspace);
+  LaunchCtx c{};
+  TP_TRY(make_launch_ctx(stream, true, &c));
+  return launch_attention_scored_bwd(c, a);
 }
 
 }  // extern "C"

@@ -1,0 +1,72 @@
+"""Refusals of the scored attention calls, without a GPU."""
+
+import pytest
+
+import megatron_tensor_sharded_b200 as tp
+
+B = [0x100000000 * i for i in range(1, 16)]   # never dereferenced
+
+
+def test_mask_refusals():
+    n = tp.tp_attention_mask_size(300)
+    assert n > 0 and tp.tp_attention_mask_size(-1) == 0 and tp.tp_attention_mask_size(2 ** 31) == 0
+
+    def mask(**kw):
+        a = dict(doc_offsets=B[0], n_docs=3, prefix=None, causal=True, mask=B[1], mask_bytes=n, T=300,
+                 stream=0, check=False)
+        a.update(kw)
+        return tp.tp_attention_mask(**a)
+
+    for kw, status in ((dict(T=-1), 1), (dict(T=2 ** 31), 4), (dict(n_docs=0), 1), (dict(doc_offsets=None), 1),
+                       (dict(prefix=B[2], causal=False), 1), (dict(doc_offsets=B[0] + 2), 3),
+                       (dict(prefix=B[2] + 1), 3), (dict(mask=None), 7), (dict(mask_bytes=n - 1), 7),
+                       (dict(mask=B[1] + 16), 3), (dict(doc_offsets=B[1] + 64), 1)):
+        assert mask(**kw) == status, kw
+    assert mask(T=0, doc_offsets=None, mask=None) == 0
+
+
+LAYOUT = [(dict(p=0), 1), (dict(T=-1), 1), (dict(n_heads=3), 2), (dict(n_kv_heads=3), 2),
+          (dict(n_heads=4, n_kv_heads=8), 1), (dict(n_heads=0), 1), (dict(head_dim=64), 4),
+          (dict(T=2 ** 31 - 1), 4)]
+SCORES = [dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(softcap=-1.0),
+          dict(softcap=float("nan"))]
+
+
+def _scores():
+    out = [(dict(score=tp.score_params(**kw)), 1) for kw in SCORES]
+    out += [(dict(score=tp.score_params(slopes=B[9] + 2)), 3), (dict(score=tp.score_params(mask=B[9] + 8)), 3),
+            (dict(score=tp.score_params(softcap=1e-5)), 4), (dict(score=tp.score_params(softcap=1e7)), 4)]
+    return out
+
+
+@pytest.mark.parametrize("kw,status", LAYOUT + _scores() + [
+    (dict(Q=None), 1), (dict(K=None), 1), (dict(V=None), 1), (dict(O=None), 1), (dict(Q=B[0] + 8), 3),
+    (dict(O=B[3] + 2), 3), (dict(LSE=B[4] + 2), 3), (dict(O=B[0]), 1), (dict(O=B[2] + 256), 1),
+    (dict(LSE=B[3]), 1), (dict(LSE=B[9], score=tp.score_params(slopes=B[9])), 1)])
+def test_forward_refusals(kw, status):
+    a = dict(Q=B[0], K=B[1], V=B[2], O=B[3], LSE=B[4], T=300, p=2, n_heads=8, n_kv_heads=4, head_dim=128,
+             score=None, stream=0, check=False)
+    a.update(kw)
+    assert tp.tp_attention_scored(**a) == status
+
+
+@pytest.mark.parametrize("kw,status", LAYOUT + _scores() + [
+    (dict(dO=None), 1), (dict(LSE=None), 1), (dict(dQ=None), 1), (dict(dV=B[8] + 8), 3), (dict(dQ=B[0]), 1),
+    (dict(dK=B[8]), 1), (dict(workspace=None), 7), (dict(workspace_bytes=8), 7), (dict(workspace=B[10] + 16), 3),
+    (dict(workspace=B[5]), 1), (dict(LSE=B[4] + 1), 3)])
+def test_backward_refusals(kw, status):
+    a = dict(Q=B[0], K=B[1], V=B[2], O=B[3], LSE=B[4], dO=B[5], dQ=B[6], dK=B[7], dV=B[8], workspace=B[10],
+             workspace_bytes=tp.tp_attention_scored_backward_workspace_size(300, 2, 8, 4, 128), T=300, p=2,
+             n_heads=8, n_kv_heads=4, head_dim=128, score=None, stream=0, check=False)
+    a.update(kw)
+    assert tp.tp_attention_scored_backward(**a) == status
+
+
+def test_nothing_to_do():
+    n0 = tp.tp_kernel_launch_count()
+    assert tp.tp_attention_scored(None, None, None, None, None, 0, 1, 1, 1, 128, stream=0, check=False) == 0
+    assert tp.tp_attention_scored_backward(None, None, None, None, None, None, None, None, None, None, 0, 0, 1, 1, 1,
+                                           128, stream=0, check=False) == 0
+    assert tp.tp_kernel_launch_count() == n0
+    assert tp.tp_attention_scored_backward_workspace_size(0, 1, 1, 1, 128) > 0
+    assert tp.tp_attention_scored_backward_workspace_size(10, 1, 1, 1, 64) == 0

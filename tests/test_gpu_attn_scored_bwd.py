@@ -1,0 +1,209 @@
+"""GPU parity of tp_attention_scored_backward against the oracle in 64 bits.
+
+The call is given O (rounded to bf16) and LSE (fp32) of the oracle's own
+forward, so only the backward is measured, against the formula with those D and
+LSE.  u = 2^-8.  With E the bound of a score's error (scored_util), P is off by
+P (2 E + 2^-22 |LSE|), then by u P when it is rounded; dP by 2^-17 sum|dO||v|
+(fp32 sums of exact products), D by 2^-17 sum|dO||O|, 1 - t^2 by 2^-18; dS is
+rounded by u.  The tile products add in fp32: 2^-13 of the sum of magnitudes is
+above their rounding for these lengths.  Every gradient is rounded once:
+    |dV - ref| <= (u + 2E + 2^-13) sum_i P |dO_i| + u |dV|
+    |dQ - ref| <= scale sum_j err(dS_ij) |k_j| + u |dQ|      (dK likewise),
+    err(dS) = P [(u + 2E + 2^-13) |dP - D| + 2^-17 (sum|dO||v| + sum|dO||O|)]
+              + 2^-18 P |dP - D|.
+Against the true gradient (D and P from exact O and LSE) the error stays within
+four roundings (P, dS, O, the result) in the 2-norm: 4 u."""
+
+import numpy as np
+import pytest
+import torch
+
+import megatron_tensor_sharded_b200 as tp
+import scored_util as S
+from oracle import attn_oracle as A
+
+pytestmark = pytest.mark.gpu
+
+
+def _forward(case, Q, K, V, seen, slopes):
+    p, T, hq, hk = case["p"], case["T"], case["h"] // case["p"], case["hkv"] // case["p"]
+    O, LSE = np.zeros_like(Q), np.zeros((p, hq, T))
+    for i in range(p):
+        for j in range(hq):
+            k, v = S.head(K, i, j * hk // hq), S.head(V, i, j * hk // hq)
+            o, lse = A.scored_head(S.head(Q, i, j), k, v, seen, S.case_scale(case), case.get("cap", 0.0), slopes[i * hq + j])
+            S.head(O, i, j)[:] = o
+            LSE[i, j] = lse
+    return O, LSE
+
+
+def _setup(case, seed=0):
+    p, T, h, hkv = case["p"], case["T"], case["h"], case["hkv"]
+    rng = np.random.default_rng(seed + T)
+    std = case.get("std", 1.0)
+    dev, host = zip(*(S.bf16(rng, p, T, n // p * 128, std=s) for n, s in ((h, std), (hkv, std), (hkv, 1.0), (h, 1.0))))
+    slopes, slopes_h = S.slopes_of(case, h)
+    score, seen, inside = S.make_score(case, slopes)
+    Q, K, V, dO = host
+    O, LSE = _forward(case, Q, K, V, seen, slopes_h)
+    O = torch.from_numpy(O).cuda().bfloat16()
+    LSE = torch.from_numpy(np.where(inside, LSE, 123.0)).cuda().float()
+    return dev, host, slopes_h, score, seen, inside, O, LSE
+
+
+def _call(case, dev, score, O, LSE):
+    p, T, h, hkv = case["p"], case["T"], case["h"], case["hkv"]
+    Q, K, V, dO = dev
+    g = [torch.full_like(x, 7.0) for x in (Q, K, V)]
+    n = tp.tp_attention_scored_backward_workspace_size(T, p, h, hkv, 128)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    tp.tp_attention_scored_backward(Q, K, V, O, LSE, dO, *g, ws, n, T, p, h, hkv, 128, score)
+    tp.tp_sync_status()
+    return g
+
+
+def _check(case, host, slopes, seen, inside, O, LSE, grads, rows=None):
+    p, T, hq, hk = case["p"], case["T"], case["h"] // case["p"], case["hkv"] // case["p"]
+    Q, K, V, dO = host
+    O, LSE = O.double().cpu().numpy(), LSE.double().cpu().numpy()
+    got = [x.double().cpu().numpy() for x in grads]
+    scale, cap, group = S.case_scale(case), case.get("cap", 0.0), hq // hk
+    rows = inside if rows is None else rows
+    u = S.U
+    for i in range(p):
+        for n in range(hk):
+            k, v = S.head(K, i, n), S.head(V, i, n)
+            sums = [np.zeros((T, 128)) for _ in range(4)]     # dk, dv and their bounds
+            for j in range(n * group, n * group + group):
+                q, do, o = S.head(Q, i, j), S.head(dO, i, j), S.head(O, i, j)
+                sl, lse = slopes[i * hq + j], LSE[i, j][:, None]
+                E = 2 * S.score_error(q, k, scale, cap, sl, T) + 2.0 ** -22 * np.abs(np.where(inside[:, None], lse, 0)).max()
+                z, t = A.scores(q, k, scale, cap, sl)
+                P = np.where(seen, np.exp(np.where(seen, z - lse, 0.0)), 0.0)
+                d = do @ v.T - (do * o).sum(1, keepdims=True)
+                mag = np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o)).sum(1, keepdims=True)
+                f = 1.0 if t is None else 1 - t * t
+                rel = u + E + 2.0 ** -13
+                dS, err = P * d * f, P * f * (rel * np.abs(d) + 2.0 ** -17 * mag) + 2.0 ** -18 * P * np.abs(d)
+                want, tol = scale * dS @ k, scale * err @ np.abs(k)
+                a = S.head(got[0], i, j)
+                assert np.all((np.abs(a - want) <= tol + u * np.abs(want))[rows & inside]), ("dQ", i, j)
+                assert np.all(a[~inside] == 7.0)
+                for x, y in zip(sums, (scale * dS.T @ q, P.T @ do, scale * err.T @ np.abs(q), rel * P.T @ np.abs(do))):
+                    x += y
+            for name, a, want, tol in (("dK", S.head(got[1], i, n), sums[0], sums[2]), ("dV", S.head(got[2], i, n), sums[1], sums[3])):
+                assert np.all((np.abs(a - want) <= tol + u * np.abs(want))[rows & inside]), (name, i, n)
+                assert np.all(a[~inside] == 7.0)
+
+
+SMALL = [(c, i) for c, i in zip(S.CASES, S.IDS) if c["h"] < 32]
+
+
+@pytest.mark.parametrize("case", [c for c, _ in SMALL], ids=[i for _, i in SMALL])
+def test_matches_oracle(case):
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    grads = _call(case, dev, score, O, LSE)
+    _check(case, host, slopes, seen, inside, O, LSE, grads)
+    again = _call(case, dev, score, O, LSE)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+@pytest.mark.parametrize("case", [
+    dict(p=1, T=1300, h=16, hkv=2, off=[0, 300, 900, 1290], cap=50.0),
+    dict(p=2, T=1100, h=8, hkv=2, cap=30.0), dict(p=1, T=900, h=4, hkv=4, slopes=1.0),
+    dict(p=1, T=1500, h=6, hkv=1, causal=False), dict(p=1, T=600, h=8, hkv=8, off=[0, 600], pre=[333], slopes=1.0, cap=20.0)])
+def test_forward_then_backward_gives_the_true_gradient(case):
+    p, T, h, hkv = case["p"], case["T"], case["h"], case["hkv"]
+    dev, host, slopes, score, seen, inside, _, _ = _setup(case, seed=3)
+    O, LSE = torch.zeros_like(dev[0]), torch.zeros(p, h // p, T, device="cuda")
+    tp.tp_attention_scored(dev[0], dev[1], dev[2], O, LSE, T, p, h, hkv, 128, score)
+    got = [x.double().cpu().numpy() for x in _call(case, dev, score, O, LSE)]
+    hq, hk = h // p, hkv // p
+    want = [np.zeros_like(x) for x in host[:3]]
+    for i in range(p):
+        for j in range(hq):
+            n = j * hk // hq
+            g = A.scored_head_backward(S.head(host[0], i, j), S.head(host[1], i, n), S.head(host[2], i, n),
+                                       S.head(host[3], i, j), seen, S.case_scale(case), case.get("cap", 0.0), slopes[i * hq + j])
+            S.head(want[0], i, j)[:] = g[0]
+            S.head(want[1], i, n)[:] += g[1]
+            S.head(want[2], i, n)[:] += g[2]
+    for a, b in zip(got, want):
+        a, b = a[:, inside], b[:, inside]
+        assert np.linalg.norm(a - b) <= 4 * S.U * np.linalg.norm(b)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_seen_adds_nothing(value):
+    """Garbage in the rows of no document and in one whole document: the other
+    document's gradients are as ever."""
+    case = dict(p=1, T=400, h=4, hkv=2, off=[0, 150, 310, 390], cap=30.0)
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    broken = ~inside
+    broken[150:310] = True
+    at = torch.from_numpy(broken).cuda()
+    for x in (*dev, O):
+        x[:, at] = value
+    LSE[..., at] = value
+    grads = _call(case, dev, score, O, LSE)
+    O, LSE = O.clone(), LSE.clone()
+    O[:, at] = 0
+    LSE[..., at] = 0
+    _check(case, host, slopes, seen, inside, O, LSE, grads, rows=~broken)
+
+
+def test_a_visible_nan_is_not_lost():
+    """One query row's upstream gradient is NaN: dK and dV of every key that
+    it sees, and its own dQ; one NaN query row: the same."""
+    T = 300
+    case = dict(p=1, T=T, h=2, hkv=1, off=[0, T])
+    for what in ("dO", "Q"):
+        for row in (5, 130, 131, 132, 133, 134, 135, 136, 137, 299):
+            dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+            (dev[3] if what == "dO" else dev[0])[0, row, 3] = float("nan")
+            dQ, dK, dV = _call(case, dev, score, O, LSE)
+            assert torch.isnan(dQ[0, row, :128]).all() and torch.isfinite(dQ[0, :row]).all()
+            assert torch.isnan(dK[0, :row + 1]).all() and torch.isfinite(dK[0, row + 1:]).all()
+            assert torch.isnan(dV[0, :row + 1, 3]).all() and torch.isfinite(dV[0, row + 1:]).all()
+
+
+def test_captured_with_the_forward():
+    case = dict(p=2, T=500, h=8, hkv=4, cap=50.0, off=[0, 211, 480])
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    T, p, h, hkv = case["T"], case["p"], case["h"], case["hkv"]
+    g = [torch.zeros_like(x) for x in dev[:3]]
+    n = tp.tp_attention_scored_backward_workspace_size(T, p, h, hkv, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def step():
+        tp.tp_attention_scored(dev[0], dev[1], dev[2], O, LSE, T, p, h, hkv, 128, score)
+        tp.tp_attention_scored_backward(dev[0], dev[1], dev[2], O, LSE, dev[3], *g, ws, n, T, p, h, hkv, 128, score)
+
+    step()
+    want = [x.clone() for x in g]
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        step()
+        for x in g:       # a torch kernel right behind the call sees its results
+            x.mul_(2)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, 2 * b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("launch", [0])
+def test_a_dropped_load_times_out(launch):
+    case = dict(p=1, T=300, h=1, hkv=1, cap=30.0)
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    tp.tp_set_wait_timeout_ns(50_000_000)
+    try:
+        tp.tp_debug_drop_load(1)
+        with pytest.raises(tp.TPError) as e:
+            _call(case, dev, score, O, LSE)
+        assert e.value.name == "TP_ERR_DEVICE_TIMEOUT"
+    finally:
+        tp.tp_set_wait_timeout_ns(0)
+        tp.tp_debug_drop_load(-1)
+    _check(case, host, slopes, seen, inside, O, LSE, _call(case, dev, score, O, LSE))
