@@ -691,9 +691,46 @@ tp_status tp_attention_scored_backward(const void* Q, const void* K, const void*
 size_t tp_attention_scored_backward_workspace_size(int64_t T, int p, int n_heads, int n_kv_heads,
                                                    int head_dim);
 
+/*
+ * Scored attention of one new token per sequence over its cache of keys and
+ * values, every shard's own heads; optionally the token's key and value are
+ * appended first (in the same pass).  With n_b = lengths[b], plus 1 when K_new
+ * and V_new are given:
+ *   K_cache[i][b][lengths[b]] = K_new[i][b] (V likewise), then
+ *   O[i][b] = softmax over keys j < n_b of
+ *             cap tanh(scale q.k_j / cap) - slope (n_b - 1 - j),  times v_j.
+ *   Q                 [p][B][(n_heads/p) * head_dim]               bf16
+ *   K_new, V_new      [p][B][(n_kv_heads/p) * head_dim]            bf16, or
+ *                     both NULL: the cache holds the token already
+ *   K_cache, V_cache  [p][B][capacity][(n_kv_heads/p) * head_dim]  bf16
+ *   lengths           [B] int32 device: keys in the cache before the call.
+ *                     n_b = 0 gives O = 0 and LSE = -inf; a negative length
+ *                     marks an unused slot: its rows of O and LSE are left
+ *                     as they were and nothing is appended.  So is a
+ *                     sequence whose n_b exceeds the capacity; tp_sync_status
+ *                     then reports TP_ERR_INVALID_ARG.
+ *   O                 as Q;  LSE [p][n_heads/p][B] fp32 or NULL
+ *   score             NULL or scale, softcap, slopes; its mask must be NULL
+ *                     (TP_ERR_UNSUPPORTED), causal is not read
+ *   workspace         tp_attention_decode_workspace_size(...) bytes, 256-byte
+ *                     aligned (partial results)
+ * Cache rows from n_b on are never read.  head_dim 128.  Reproducible.
+ */
+tp_status tp_attention_decode(const void* Q, const void* K_new, const void* V_new, void* K_cache,
+                              void* V_cache, const int32_t* lengths, void* O, float* LSE,
+                              void* workspace, size_t workspace_bytes, int64_t B,
+                              int64_t capacity, int p, int n_heads, int n_kv_heads, int head_dim,
+                              const tp_score_params* score, void* stream);
+
+/* Workspace bytes tp_attention_decode needs (0 if the arguments are invalid). */
+size_t tp_attention_decode_workspace_size(int64_t B, int64_t capacity, int p, int n_heads,
+                                          int n_kv_heads, int head_dim);
+
 /* Synchronise `stream`, then report (and clear) the device status word of
  * the current device: TP_ERR_DEVICE_TIMEOUT if a bounded wait ran out since
- * the last call, TP_ERR_CUDA if the stream reported an error, else TP_OK. */
+ * the last call, TP_ERR_INVALID_ARG if tp_attention_decode met a length that
+ * its cache does not hold, TP_ERR_CUDA if the stream reported an error, else
+ * TP_OK. */
 tp_status tp_sync_status(void* stream);
 
 /* Limit for every bounded device-side wait, in nanoseconds (default 2e9).

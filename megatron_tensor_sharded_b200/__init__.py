@@ -61,7 +61,8 @@ __all__ = [
     # attention with capped, biased and masked scores
     "ScoreParams", "score_params", "tp_attention_mask", "tp_attention_mask_size",
     "tp_attention_scored", "tp_attention_scored_backward",
-    "tp_attention_scored_backward_workspace_size",
+    "tp_attention_scored_backward_workspace_size", "tp_attention_decode",
+    "tp_attention_decode_workspace_size",
     # the all-reduce of partials held on p GPUs
     "TP_GATHER_MAX", "IpcHandle", "tp_reduce_partials_gather", "tp_ipc_export", "tp_ipc_import",
     "tp_ipc_release",
@@ -201,6 +202,9 @@ def _load() -> ctypes.CDLL:
     lib.tp_attention_scored_backward.argtypes = [vp] * 10 + [sz, i64, i32, i32, i32, i32, score, vp]
     lib.tp_attention_scored_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
     lib.tp_attention_scored_backward_workspace_size.restype = sz
+    lib.tp_attention_decode.argtypes = [vp] * 9 + [sz, i64, i64, i32, i32, i32, i32, score, vp]
+    lib.tp_attention_decode_workspace_size.argtypes = [i64, i64, i32, i32, i32, i32]
+    lib.tp_attention_decode_workspace_size.restype = sz
     lib.tp_ipc_export.argtypes = [vp, ctypes.POINTER(IpcHandle)]
     lib.tp_ipc_import.argtypes = [ctypes.POINTER(IpcHandle), ctypes.POINTER(vp)]
     lib.tp_ipc_release.argtypes = [ctypes.POINTER(IpcHandle)]
@@ -218,7 +222,8 @@ def _load() -> ctypes.CDLL:
               "tp_debug_exp2_poly", "tp_reduce_partials_gather", "tp_ipc_export",
               "tp_ipc_import", "tp_ipc_release", "tp_rope_plan_init", "tp_rope",
               "tp_qk_norm_rope", "tp_qk_norm_rope_backward", "tp_attention_mask",
-              "tp_attention_scored", "tp_attention_scored_backward"):
+              "tp_attention_scored", "tp_attention_scored_backward",
+              "tp_attention_decode"):
         getattr(lib, f).restype = i32
     return lib
 
@@ -518,6 +523,21 @@ def tp_attention_scored_backward(Q, K, V, O, LSE, dO, dQ, dK, dV, workspace, wor
 
 def tp_attention_scored_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim) -> int:
     return int(_lib.tp_attention_scored_backward_workspace_size(T, p, n_heads, n_kv_heads, head_dim))
+
+
+def tp_attention_decode(Q, K_new, V_new, K_cache, V_cache, lengths, O, LSE, workspace,
+                        workspace_bytes, B, capacity, p, n_heads, n_kv_heads, head_dim, score=None,
+                        stream=None, check=True):
+    """Scored attention of one new token per sequence over its cache; K_new and
+    V_new (or None) are appended at lengths[b] first."""
+    return _check(_lib.tp_attention_decode(
+        _ptr(Q), _ptr(K_new), _ptr(V_new), _ptr(K_cache), _ptr(V_cache), _ptr(lengths), _ptr(O),
+        _ptr(LSE), _ptr(workspace), workspace_bytes, B, capacity, p, n_heads, n_kv_heads, head_dim,
+        score, _stream(stream)), check)
+
+
+def tp_attention_decode_workspace_size(B, capacity, p, n_heads, n_kv_heads, head_dim) -> int:
+    return int(_lib.tp_attention_decode_workspace_size(B, capacity, p, n_heads, n_kv_heads, head_dim))
 
 
 def tp_debug_exp2_poly(x, y, n, stream=None, check=True):

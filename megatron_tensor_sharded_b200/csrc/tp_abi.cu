@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <mutex>
 
+#include "tp_device.cuh"
 #include "tp_internal.h"
 #include "tp_launch.cuh"
 #include "tp_mlp.h"
@@ -905,6 +906,8 @@ tp_status tp_sync_status(void* stream) {
     const unsigned zero = 0;
     e = cudaMemcpyToSymbol(g_tp_status_word, &zero, sizeof(zero));
     if (e != cudaSuccess) return fail(TP_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
+    if (word == kErrLength)
+      return fail(TP_ERR_INVALID_ARG, "a sequence's length exceeds its cache");
     return fail(TP_ERR_DEVICE_TIMEOUT, "device wait gave up (status bits 0x%x)", word);
   }
   return TP_OK;

@@ -183,6 +183,24 @@ size_t score_bwd_ws(const ScoreCall& a) {
   return align256(static_cast<size_t>(a.T) * a.p * a.hq * 4);
 }
 
+// Sizes and options of a decode call into `a` (its T is the batch).
+tp_status decode_sizes(ScoreCall* a, int64_t B, int64_t capacity, int p, int n_heads,
+                       int n_kv_heads, int head_dim, const tp_score_params* s) {
+  TP_TRY(score_call(a, B, p, n_heads, n_kv_heads, head_dim, s));
+  if (a->mask != nullptr)
+    TP_FAIL(TP_ERR_UNSUPPORTED, "a single token's call takes lengths, not a mask");
+  if (capacity < 1) TP_FAIL(TP_ERR_INVALID_ARG, "capacity = %lld", (long long)capacity);
+  if (capacity > (int64_t(1) << 30) || B > (1 << 20) || B * n_heads > (int64_t(1) << 30) ||
+      B * n_kv_heads * capacity > (int64_t(1) << 44))
+    TP_FAIL(TP_ERR_UNSUPPORTED, "sizes too large (B = %lld, capacity = %lld)", (long long)B,
+            (long long)capacity);
+  return TP_OK;
+}
+size_t decode_ws(const ScoreCall& a, int64_t B, int64_t capacity) {
+  // (for any number of SMs: the caller may ask on a machine without a GPU)
+  return align256(decode_part_bytes(decode_ctas(kMaxDecodeCtas, B, capacity, a.p, a.hq, a.hkv)));
+}
+
 tp_status check_bf16(const void* p, const char* name) {
   if (p == nullptr) TP_FAIL(TP_ERR_INVALID_ARG, "%s is NULL", name);
   if (!aligned(p, 16)) TP_FAIL(TP_ERR_ALIGNMENT, "%s must be 16-byte aligned", name);
@@ -475,6 +493,72 @@ tp_status tp_attention_scored_backward(const void* Q, const void* K, const void*
   LaunchCtx c{};
   TP_TRY(make_launch_ctx(stream, true, &c));
   return launch_attention_scored_bwd(c, a);
+}
+
+size_t tp_attention_decode_workspace_size(int64_t B, int64_t capacity, int p, int n_heads,
+                                          int n_kv_heads, int head_dim) {
+  ScoreCall a{};
+  if (decode_sizes(&a, B, capacity, p, n_heads, n_kv_heads, head_dim, nullptr) != TP_OK) return 0;
+  return B == 0 ? 256 : decode_ws(a, B, capacity);
+}
+
+tp_status tp_attention_decode(const void* Q, const void* K_new, const void* V_new, void* K_cache,
+                              void* V_cache, const int32_t* lengths, void* O, float* LSE,
+                              void* workspace, size_t workspace_bytes, int64_t B,
+                              int64_t capacity, int p, int n_heads, int n_kv_heads, int head_dim,
+                              const tp_score_params* score, void* stream) {
+  set_error_detail("%s", "");
+  ScoreCall a{};
+  TP_TRY(decode_sizes(&a, B, capacity, p, n_heads, n_kv_heads, head_dim, score));
+  if (B == 0) return TP_OK;
+  TP_TRY(check_bf16(Q, "Q"));
+  if ((K_new == nullptr) != (V_new == nullptr))
+    TP_FAIL(TP_ERR_INVALID_ARG, "K_new and V_new are given together or not at all");
+  if (K_new != nullptr) {
+    TP_TRY(check_bf16(K_new, "K_new"));
+    TP_TRY(check_bf16(V_new, "V_new"));
+  }
+  TP_TRY(check_bf16(K_cache, "K_cache"));
+  TP_TRY(check_bf16(V_cache, "V_cache"));
+  TP_TRY(check_bf16(O, "O"));
+  if (lengths == nullptr) TP_FAIL(TP_ERR_INVALID_ARG, "lengths is NULL");
+  if (!aligned(lengths, 4) || !aligned(LSE, 4))
+    TP_FAIL(TP_ERR_ALIGNMENT, "lengths and LSE must be 4-byte aligned");
+  const size_t need = decode_ws(a, B, capacity);
+  TP_TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t b = static_cast<size_t>(B), q = b * n_heads * 256, kv = b * n_kv_heads * 256;
+  const size_t cache = kv * static_cast<size_t>(capacity);
+  TP_TRY(check_overlaps({{"O", O, q, nullptr},
+                         {"LSE", LSE, b * n_heads * 4, nullptr},
+                         {"K_cache", K_cache, cache, nullptr},
+                         {"V_cache", V_cache, cache, nullptr},
+                         {"workspace", workspace, need, nullptr}},
+                        {{"Q", Q, q, nullptr},
+                         {"K_new", K_new, kv, nullptr},
+                         {"V_new", V_new, kv, nullptr},
+                         {"lengths", lengths, b * 4, nullptr},
+                         {"slopes", a.slopes, static_cast<size_t>(n_heads) * 4, nullptr}}));
+  DecodeCall d{};
+  d.Q = Q;
+  d.Kn = K_new;
+  d.Vn = V_new;
+  d.Kc = K_cache;
+  d.Vc = V_cache;
+  d.O = O;
+  d.LSE = LSE;
+  d.part = static_cast<float*>(workspace);
+  d.len = lengths;
+  d.B = B;
+  d.capacity = capacity;
+  d.p = a.p;
+  d.hq = a.hq;
+  d.hkv = a.hkv;
+  d.scale = a.scale;
+  d.cap = a.cap;
+  d.slopes = a.slopes;
+  LaunchCtx c{};
+  TP_TRY(make_launch_ctx(stream, false, &c));
+  return launch_attention_decode(c, d);
 }
 
 }  // extern "C"

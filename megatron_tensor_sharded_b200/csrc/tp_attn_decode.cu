@@ -1,0 +1,580 @@
+// Scored attention of one new token per sequence over its key/value cache.
+//
+// Bound by HBM: every cached key and value in sight is read once (512 bytes a
+// key and key/value head), 4 * 128 flops a key and query head.  So the work
+// is cut by bytes, not by rows: all (sequence, shard, key/value head) items'
+// 64-key tiles form one line, which the CTAs share out evenly; a CTA walks its
+// stretch without a pause between items.  An item that ends up on several
+// CTAs leaves one partial (max, sum, O) each, and decode_join_kernel adds them
+// in the order of the CTAs: the same bits on every run.
+//
+// A group's query heads (padded to the 16 rows of an MMA tile; more than 16
+// heads take several items that share their cache lines through L2) run
+// together, so the cache is read once for all of them.  Each of the four warps
+// has its own 16 keys of a tile and its own three-slot ring, filled by
+// 16-byte asynchronous copies, with its own running maximum: no barrier in
+// the loop.  The products are warp-level MMAs (m16n8k16): a tensor-core tile
+// of 128 rows would be nearly empty here, and the arithmetic is a tenth of
+// what the copies take.  Two CTAs an SM keep up to 192 KB in flight.
+//
+// Keys behind a sequence's length are never read (their copies are zero
+// filled) and masked; the appended key and value come from the call's K_new
+// and V_new and are written to the cache by the warp that uses them.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "tp_device.cuh"
+#include "tp_internal.h"
+#include "tp_launch.cuh"
+#include "tp_score.h"
+#include "tp_softmax.cuh"
+
+namespace tpk {
+namespace {
+
+constexpr int DH = 128;
+constexpr int TILE = 64;                 // keys of a tile, 16 a warp
+constexpr int WARPS = 4;
+constexpr int NST = 3;                   // ring slots of a warp
+constexpr int MROWS = 16;                // query heads of an item
+constexpr int WTILE_BYTES = 16 * DH * 2; // a warp's keys (or values) of a tile
+constexpr int RING_BYTES = WARPS * NST * 2 * WTILE_BYTES;
+constexpr int SMEM_BYTES = RING_BYTES + MROWS * DH * 4 + 2 * WARPS * MROWS * 4;
+constexpr int CTAS_PER_SM = 2;
+constexpr int PART_FLOATS = MROWS * (DH + 2);   // O rows, then max and sum of each
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct DecodeParams {
+  const __nv_bfloat16 *Q, *Kn, *Vn;
+  __nv_bfloat16 *Kc, *Vc, *O;
+  float *LSE, *part;
+  const int32_t* len;
+  const float* slopes;
+  int32_t B, p, hq, hkv, group, mtiles, heads, ctas;   // heads: items of a sequence
+  int64_t capacity;
+  ScoreConsts s;
+  unsigned* err;
+};
+
+// Keys in sight of sequence b's token, the appended one included; -1: the
+// slot is unused, -2: the length does not fit the cache.
+__device__ __forceinline__ int32_t keys_of(const DecodeParams& P, int32_t b) {
+  const int32_t n = P.len[b];
+  if (n < 0) return -1;
+  const int64_t keys = static_cast<int64_t>(n) + (P.Kn != nullptr ? 1 : 0);
+  return keys > P.capacity ? -2 : static_cast<int32_t>(keys);
+}
+__device__ __forceinline__ int64_t tiles_of(int32_t keys) {
+  return keys <= 0 ? 0 : (keys + TILE - 1) / TILE;
+}
+
+// Sum of v over the CTA's threads; every thread gets it (and, in *before, the
+// sum over the threads of a lower number).
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* before, int64_t* scratch) {
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (threadIdx.x % 32 >= o) x += y;
+  }
+  __syncthreads();
+  if (threadIdx.x % 32 == 31) scratch[threadIdx.x / 32] = x;
+  __syncthreads();
+  int64_t total = 0, base = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
+    if (w < static_cast<int>(threadIdx.x) / 32) base += scratch[w];
+    total += scratch[w];
+  }
+  *before = base + x - v;
+  return total;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(read ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16-byte chunk c of row r of a warp's 16 x 256-byte tile, swizzled so that
+// eight rows' chunks of one column lie in different banks.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
+  return tile + r * 256 + ((c ^ (r & 7)) * 16);
+}
+
+// Where a CTA stands on the line of tiles.
+struct Place {
+  int32_t b, h, keys;     // sequence, item of it, its keys
+  int64_t tile, tiles;    // tile of the item
+};
+__device__ __forceinline__ void advance(const DecodeParams& P, Place& x) {
+  if (++x.tile < x.tiles) return;
+  x.tile = 0;
+  if (++x.h < P.heads) return;
+  x.h = 0;
+  do {
+    if (++x.b >= P.B) return;
+    x.keys = keys_of(P, x.b);
+    x.tiles = tiles_of(x.keys);
+  } while (x.tiles == 0);
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
+    decode_kernel(const __grid_constant__ DecodeParams P) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scratch[WARPS];
+  __shared__ Place start;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t ring = smem_u32(smem) + warp * NST * 2 * WTILE_BYTES;
+  float* const sum_o = reinterpret_cast<float*>(smem + RING_BYTES);          // [16][128]
+  float* const warp_m = sum_o + MROWS * DH;                                  // [warp][16]
+  float* const warp_l = warp_m + WARPS * MROWS;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // The line's length, then the place of this CTA's first tile on it.
+  int64_t total = 0, before;
+  bool bad = false;
+  for (int32_t b0 = 0; b0 < P.B; b0 += WARPS * 32) {
+    const int32_t b = b0 + threadIdx.x;
+    const int32_t keys = b < P.B ? keys_of(P, b) : 0;
+    bad |= keys == -2;
+    total += block_sum(tiles_of(keys) * P.heads, &before, scratch);
+  }
+  if (bad && blockIdx.x == 0) atomicOr(P.err, kErrLength);
+  const int64_t w0 = total * blockIdx.x / P.ctas, w1 = total * (blockIdx.x + 1) / P.ctas;
+  if (w0 >= w1) return;
+  int64_t done = 0;
+  for (int32_t b0 = 0; b0 < P.B && done <= w0; b0 += WARPS * 32) {
+    const int32_t b = b0 + threadIdx.x;
+    const int32_t keys = b < P.B ? keys_of(P, b) : 0;
+    const int64_t tiles = tiles_of(keys), mine = tiles * P.heads;
+    const int64_t sum = block_sum(mine, &before, scratch);
+    const int64_t at = w0 - (done + before);
+    if (mine > 0 && at >= 0 && at < mine)
+      start = Place{b, static_cast<int32_t>(at / tiles), keys, at % tiles, tiles};
+    done += sum;
+  }
+  __syncthreads();
+  Place use = start, get = start;
+
+  // Copies of one tile of the walk into ring slot st (nothing past w1).
+  auto fetch = [&](int64_t w, int st) {
+    if (w < w1) {
+      const int32_t hk = get.h / P.mtiles;
+      const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
+      const int64_t key0 = get.tile * TILE + warp * 16;
+      const int64_t pitch = static_cast<int64_t>(P.hkv) * DH;
+      const int64_t seq = static_cast<int64_t>(shard) * P.B + get.b;
+      const int64_t off = (seq * P.capacity + key0) * pitch + kvh * DH;
+      const int64_t off_new = seq * pitch + kvh * DH;
+      const int fresh = P.Kn != nullptr ? get.keys - 1 - static_cast<int>(key0) : -1;
+      const int left = get.keys - static_cast<int>(key0);
+      const uint32_t kt = ring + st * 2 * WTILE_BYTES, vt = kt + WTILE_BYTES;
+      const int c = lane % 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 2 + lane / 16;
+        const bool own = r == fresh, read = r < left;
+        // (an address in range also where nothing is read)
+        const int64_t src = own ? off_new : off + (read ? r : 0) * pitch;
+        const __nv_bfloat16* k = (own ? P.Kn : P.Kc) + src + c * 8;
+        const __nv_bfloat16* v = (own ? P.Vn : P.Vc) + src + c * 8;
+        cp_async16(chunk_at(kt, r, c), read ? k : P.Kc, read);
+        cp_async16(chunk_at(vt, r, c), read ? v : P.Vc, read);
+        if (own && get.h % P.mtiles == 0) {
+          const int64_t to = off + r * pitch + c * 8;
+          *reinterpret_cast<uint4*>(P.Kc + to) = *reinterpret_cast<const uint4*>(k);
+          *reinterpret_cast<uint4*>(P.Vc + to) = *reinterpret_cast<const uint4*>(v);
+        }
+      }
+      advance(P, get);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+#pragma unroll
+  for (int st = 0; st < NST - 1; ++st) fetch(w0 + st, st);
+
+  uint32_t q[8][4];
+  float o[16][4], m[2], l[2], slope2[2];
+  bool first = true;        // the item at hand began before this CTA
+  bool open = false;        // q, o, m, l hold an item
+  int slot = 0;
+  for (int64_t w = w0; w < w1; ++w) {
+    if (!open) {
+      const int32_t hk = use.h / P.mtiles, mt = use.h - hk * P.mtiles;
+      const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
+      const __nv_bfloat16* Q =
+          P.Q + ((static_cast<int64_t>(shard) * P.B + use.b) * P.hq + kvh * P.group) * DH;
+      const int r0 = mt * MROWS + lane / 4, r1 = r0 + 8;   // query heads of the group
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const int d = kk * 16 + (lane % 4) * 2;
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(Q + static_cast<int64_t>(r0) * DH + d);
+        const uint32_t* b = reinterpret_cast<const uint32_t*>(Q + static_cast<int64_t>(r1) * DH + d);
+        q[kk][0] = r0 < P.group ? a[0] : 0u;
+        q[kk][1] = r1 < P.group ? b[0] : 0u;
+        q[kk][2] = r0 < P.group ? a[4] : 0u;
+        q[kk][3] = r1 < P.group ? b[4] : 0u;
+      }
+      if (BIAS) {
+        const float* sl = P.slopes + shard * P.hq + kvh * P.group;
+        slope2[0] = r0 < P.group ? kLog2e * sl[r0] : 0.0f;
+        slope2[1] = r1 < P.group ? kLog2e * sl[r1] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.0f;
+      open = true;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+    __syncwarp();
+    fetch(w + NST - 1, slot == 0 ? NST - 1 : slot - 1);   // the slot of the tile before this one
+    const uint32_t kt = ring + slot * 2 * WTILE_BYTES, vt = kt + WTILE_BYTES;
+
+    // scores of 16 heads x 16 keys
+    float s[2][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      uint32_t k4[4];   // keys 0..7 / 8..15 by the two halves of 16 elements
+      ldsm4(k4, chunk_at(kt, (lane & 7) + ((lane >> 4) & 1) * 8, kk * 2 + ((lane >> 3) & 1)));
+      mma16816(s[0], q[kk], k4[0], k4[1]);
+      mma16816(s[1], q[kk], k4[2], k4[3]);
+    }
+    const int32_t key0 = static_cast<int32_t>(use.tile * TILE) + warp * 16;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int32_t key = key0 + n * 8 + (lane % 4) * 2 + (e & 1);
+        float z;
+        if (CAP) {
+          const float t = 1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s[n][e]) * P.s.two_x));
+          z = P.s.cap_log2 * copysignf(t, s[n][e]);
+          if (s[n][e] != s[n][e]) z = s[n][e];
+        } else {
+          z = s[n][e] * P.s.scale_log2;
+        }
+        if (BIAS) z = fmaf(slope2[e >> 1], static_cast<float>(key - (use.keys - 1)), z);
+        if (key >= use.keys) z = -INFINITY;
+        s[n][e] = z;
+        mx[e >> 1] = max3_nan(mx[e >> 1], z, z);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = max3_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1), mx[h]);
+      mx[h] = max3_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2), mx[h]);
+    }
+    const bool grow = !(mx[0] <= m[0]) || !(mx[1] <= m[1]);
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float mn = max3_nan(m[h], mx[h], mx[h]);
+        const float alpha = mn == -INFINITY ? 1.0f : ex2(m[h] - mn);
+        m[h] = mn;
+        l[h] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          o[i][2 * h] *= alpha;
+          o[i][2 * h + 1] *= alpha;
+        }
+      }
+    }
+    const float mo[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+    uint32_t pa[4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      float e4[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        e4[e] = ex2(s[n][e] - mo[e >> 1]);
+        l[e >> 1] += e4[e];
+      }
+      pa[n * 2] = pack2(e4[0], e4[1]);
+      pa[n * 2 + 1] = pack2(e4[2], e4[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t v4[4];   // keys 0..7, 8..15 of elements 16i.., then of 16i + 8..
+      ldsm4_t(v4, chunk_at(vt, (lane & 7) + ((lane >> 3) & 1) * 8, i * 2 + ((lane >> 4) & 1)));
+      mma16816(o[2 * i], pa, v4[0], v4[1]);
+      mma16816(o[2 * i + 1], pa, v4[2], v4[3]);
+    }
+    __syncwarp();   // every lane is done with the slot
+    slot = slot + 1 == NST ? 0 : slot + 1;
+
+    const bool item_ends = use.tile + 1 == use.tiles;
+    if (item_ends || w + 1 == w1) {
+      // join the warps: rows' maxima and sums, then O warp by warp
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (lane % 4 == 0) {
+          warp_m[warp * MROWS + h * 8 + lane / 4] = m[h];
+          warp_l[warp * MROWS + h * 8 + lane / 4] = l[h];
+        }
+      }
+      __syncthreads();
+      float M[2], f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        M[h] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) {
+          const float x = warp_m[i * MROWS + h * 8 + lane / 4];
+          M[h] = max3_nan(M[h], x, x);
+        }
+        f[h] = m[h] == -INFINITY ? 0.0f : ex2(m[h] - M[h]);
+      }
+      for (int i = 0; i < WARPS; ++i) {
+        if (warp == i) {
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2* at = reinterpret_cast<float2*>(sum_o + (h * 8 + lane / 4) * DH + n * 8 + (lane % 4) * 2);
+              float2 x = make_float2(o[n][2 * h] * f[h], o[n][2 * h + 1] * f[h]);
+              if (i > 0) {
+                const float2 y = *at;
+                x.x += y.x;
+                x.y += y.y;
+              }
+              *at = x;
+            }
+          }
+        }
+        __syncthreads();
+      }
+      const int32_t hk = use.h / P.mtiles, mt = use.h - hk * P.mtiles;
+      const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
+      const bool whole = item_ends && !(first && start.tile != 0);
+      const int rows = min(MROWS, P.group - mt * MROWS);
+      float* const part =
+          P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (first ? 0 : 1)) * PART_FLOATS;
+      for (int row = warp; row < rows; row += WARPS) {
+        float Mr = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) {
+          const float x = warp_m[i * MROWS + row];
+          Mr = max3_nan(Mr, x, x);
+        }
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) {
+          const float x = warp_m[i * MROWS + row];
+          if (x != -INFINITY) L += warp_l[i * MROWS + row] * ex2(x - Mr);
+        }
+        const float4 x = *reinterpret_cast<const float4*>(sum_o + row * DH + lane * 4);
+        if (whole) {
+          const int32_t head = kvh * P.group + mt * MROWS + row;
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          *reinterpret_cast<uint2*>(
+              P.O + ((static_cast<int64_t>(shard) * P.B + use.b) * P.hq + head) * DH + lane * 4) =
+              make_uint2(pack2(x.x * inv, x.y * inv), pack2(x.z * inv, x.w * inv));
+          if (P.LSE != nullptr && lane == 0)
+            P.LSE[(static_cast<int64_t>(shard) * P.hq + head) * P.B + use.b] =
+                L == 0.0f ? -INFINITY : 0.6931471805599453f * Mr + logf(L);
+        } else {
+          *reinterpret_cast<float4*>(part + row * DH + lane * 4) = x;
+          if (lane == 0) {
+            part[MROWS * DH + row] = Mr;
+            part[MROWS * DH + MROWS + row] = L;
+          }
+        }
+      }
+      __syncthreads();   // sum_o and the rows' numbers are free again
+      open = false;
+      first = false;
+    }
+    advance(P, use);
+  }
+}
+
+// Adds the partials of an item that lay on several CTAs, in their order, and
+// writes zeros for sequences without keys.  One CTA a (item, query head); eight
+// groups of lanes share the parts, then add up in order.
+constexpr int JOIN_THREADS = 256;
+__global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_constant__ DecodeParams P) {
+  __shared__ int64_t scratch[JOIN_THREADS / 32];
+  __shared__ float grp_m[8];
+  __shared__ float grp_l[8];
+  __shared__ __align__(16) float grp_o[8][DH];
+  const int32_t item = blockIdx.x;
+  const int32_t b = item / P.heads, h = item - b * P.heads;
+  const int32_t hk = h / P.mtiles, mt = h - hk * P.mtiles;
+  const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
+  const int32_t in_group = mt * MROWS + blockIdx.y;
+  if (in_group >= P.group) return;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int32_t keys = keys_of(P, b);
+  if (keys < 0) return;
+  const int32_t head = kvh * P.group + in_group, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  __nv_bfloat16* const out = P.O + ((static_cast<int64_t>(shard) * P.B + b) * P.hq + head) * DH;
+  float* const lse =
+      P.LSE != nullptr ? P.LSE + (static_cast<int64_t>(shard) * P.hq + head) * P.B + b : nullptr;
+  if (keys == 0) {
+    if (warp == 0) *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(0, 0);
+    if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
+    return;
+  }
+  int64_t total = 0, ahead = 0, before;
+  for (int32_t b0 = 0; b0 < P.B; b0 += JOIN_THREADS) {
+    const int32_t i = b0 + threadIdx.x;
+    const int64_t t = i < P.B ? tiles_of(keys_of(P, i)) * P.heads : 0;
+    total += block_sum(t, &before, scratch);
+    ahead += block_sum(i < b ? t : 0, &before, scratch);
+  }
+  const int64_t tiles = tiles_of(keys), a = ahead + h * tiles, z = a + tiles - 1;
+  // the CTA of tile w: the last c with total * c / ctas <= w
+  auto cta_of = [&](int64_t w) { return ((w + 1) * P.ctas - 1) / total; };
+  const int64_t c0 = cta_of(a), c1 = cta_of(z);
+  if (c0 == c1) return;   // written whole
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int64_t c = c0 + warp; c <= c1; c += JOIN_THREADS / 32) {
+    if (total * c / P.ctas == total * (c + 1) / P.ctas) continue;   // fewer tiles than CTAs
+    // a CTA's first item is its slot 0; the item begins inside c0 unless it
+    // begins with it
+    const bool second = c == c0 && total * c / P.ctas != a;
+    const float* part = P.part + (c * 2 + (second ? 1 : 0)) * PART_FLOATS;
+    const float pm = part[MROWS * DH + blockIdx.y], pl = part[MROWS * DH + MROWS + blockIdx.y];
+    const float4 x = *reinterpret_cast<const float4*>(part + blockIdx.y * DH + lane * 4);
+    const float mn = max3_nan(m, pm, pm);
+    const float fa = m == -INFINITY ? 0.0f : ex2(m - mn), fb = pm == -INFINITY ? 0.0f : ex2(pm - mn);
+    l = l * fa + pl * fb;
+    o.x = o.x * fa + x.x * fb;
+    o.y = o.y * fa + x.y * fb;
+    o.z = o.z * fa + x.z * fb;
+    o.w = o.w * fa + x.w * fb;
+    m = mn;
+  }
+  if (lane == 0) {
+    grp_m[warp] = m;
+    grp_l[warp] = l;
+  }
+  *reinterpret_cast<float4*>(&grp_o[warp][lane * 4]) = o;
+  __syncthreads();
+  if (threadIdx.x < DH) {
+    float M = -INFINITY, L = 0.0f, v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) M = max3_nan(M, grp_m[i], grp_m[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = grp_m[i] == -INFINITY ? 0.0f : ex2(grp_m[i] - M);
+      L += grp_l[i] * f;
+      v += grp_o[i][threadIdx.x] * f;
+    }
+    out[threadIdx.x] = __float2bfloat16_rn(L == 0.0f ? 0.0f : v / L);
+    if (threadIdx.x == 0 && lse != nullptr)
+      *lse = L == 0.0f ? -INFINITY : 0.6931471805599453f * M + logf(L);
+  }
+}
+
+template <bool CAP, bool BIAS>
+tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
+  static uint64_t attr_epoch[64] = {};
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    const int dev = c.device & 63;
+    if (attr_epoch[dev] != c.epoch) {
+      if (cudaFuncSetAttribute(decode_kernel<CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               SMEM_BYTES) != cudaSuccess) {
+        set_error_detail("cudaFuncSetAttribute failed: %s", cudaGetErrorString(cudaGetLastError()));
+        return TP_ERR_CUDA;
+      }
+      attr_epoch[dev] = c.epoch;
+    }
+  }
+  cudaError_t e = launch_pdl(decode_kernel<CAP, BIAS>, dim3(prm.ctas), dim3(WARPS * 32), SMEM_BYTES,
+                             c.stream, prm);
+  note_launch();
+  if (e == cudaSuccess) {
+    e = launch_pdl(decode_join_kernel, dim3(prm.B * prm.heads, prm.group < MROWS ? prm.group : MROWS),
+                   dim3(JOIN_THREADS), 0, c.stream, prm);
+    note_launch();
+  }
+  if (e != cudaSuccess) {
+    set_error_detail("decode launch failed: %s", cudaGetErrorString(e));
+    return TP_ERR_CUDA;
+  }
+  return TP_OK;
+}
+
+}  // namespace
+
+// CTAs that share the line of tiles: two an SM, fewer where the caches could
+// not give each a tile.
+int64_t decode_ctas(int num_sms, int64_t B, int64_t capacity, int p, int hq, int hkv) {
+  const int64_t mtiles = (hq / hkv + MROWS - 1) / MROWS;
+  const int64_t most = B * p * hkv * mtiles * ((capacity + TILE - 1) / TILE);
+  int64_t full = static_cast<int64_t>(num_sms) * CTAS_PER_SM;
+  if (full > kMaxDecodeCtas) full = kMaxDecodeCtas;
+  return most < full ? most : full;
+}
+size_t decode_part_bytes(int64_t ctas) {
+  return static_cast<size_t>(ctas) * 2 * PART_FLOATS * sizeof(float);
+}
+
+tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a) {
+  DecodeParams prm{};
+  prm.Q = static_cast<const __nv_bfloat16*>(a.Q);
+  prm.Kn = static_cast<const __nv_bfloat16*>(a.Kn);
+  prm.Vn = static_cast<const __nv_bfloat16*>(a.Vn);
+  prm.Kc = static_cast<__nv_bfloat16*>(a.Kc);
+  prm.Vc = static_cast<__nv_bfloat16*>(a.Vc);
+  prm.O = static_cast<__nv_bfloat16*>(a.O);
+  prm.LSE = a.LSE;
+  prm.part = a.part;
+  prm.len = a.len;
+  prm.slopes = a.slopes;
+  prm.B = static_cast<int32_t>(a.B);
+  prm.p = a.p;
+  prm.hq = a.hq;
+  prm.hkv = a.hkv;
+  prm.group = a.hq / a.hkv;
+  prm.mtiles = (prm.group + MROWS - 1) / MROWS;
+  prm.heads = a.p * a.hkv * prm.mtiles;
+  prm.capacity = a.capacity;
+  prm.s = score_consts(a.scale, a.cap);
+  prm.err = c.err_word;
+  prm.ctas = static_cast<int32_t>(decode_ctas(c.num_sms, a.B, a.capacity, a.p, a.hq, a.hkv));
+  const bool cap = a.cap > 0.0f, bias = a.slopes != nullptr;
+  if (cap && bias) return launch_decode<true, true>(c, prm);
+  if (cap) return launch_decode<true, false>(c, prm);
+  if (bias) return launch_decode<false, true>(c, prm);
+  return launch_decode<false, false>(c, prm);
+}
+
+}  // namespace tpk

@@ -17,6 +17,8 @@ constexpr unsigned kErrWaitAccEmpty = 1u << 3;  // mma: accumulator never draine
 constexpr unsigned kErrWaitDrain = 1u << 4;     // teardown: in-flight work never finished
 constexpr unsigned kErrWaitRegion = 1u << 7;    // fold: a region's partial tiles never completed
 
+constexpr unsigned kErrLength = 1u << 8;        // decode: a sequence longer than its cache
+
 struct WaitCtl {
   unsigned* err;        // per-device status word
   uint64_t timeout_ns;  // limit for each wait

@@ -83,6 +83,22 @@ struct ScoreCall {
   const void* mask;        // plan or null
 };
 
+struct DecodeCall {
+  const void *Q, *Kn, *Vn;   // Kn, Vn: the tokens to append, or null
+  void *Kc, *Vc, *O;
+  float *LSE, *part;         // LSE may be null; part: decode_part_bytes()
+  const int32_t* len;
+  int64_t B, capacity;
+  int p, hq, hkv;            // heads per shard
+  float scale, cap;
+  const float* slopes;
+};
+constexpr int kMaxDecodeCtas = 512;
+// CTAs of a decode call, and the bytes of their partials.
+int64_t decode_ctas(int num_sms, int64_t B, int64_t capacity, int p, int hq, int hkv);
+size_t decode_part_bytes(int64_t ctas);
+tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a);
+
 cudaError_t launch_attention_mask(const LaunchCtx& c, const int32_t* off, int n_docs,
                                   const int32_t* prefix, bool causal, void* mask, int64_t T);
 tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a);

@@ -126,3 +126,17 @@ def scored_head_backward(q, k, v, do, seen, scale, cap=0.0, slope=0.0):
         dz = dz * (1 - t * t)
     dz = dz * scale
     return dz @ k, dz.T @ q, P.T @ do
+
+
+def scored_row(q, k, v, scale, cap=0.0, slope=0.0):
+    """(o, lse) of one query behind the keys k (the last one its own)."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    n = len(k)
+    if n == 0:
+        return np.zeros(q.shape), -np.inf
+    z = scale * (k @ q)
+    if cap:
+        z = cap * np.tanh(z / cap)
+    z = z - slope * np.arange(n - 1, -1, -1)
+    e = np.exp(z - z.max())
+    return (e @ v) / e.sum(), z.max() + math.log(e.sum())

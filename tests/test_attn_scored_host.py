@@ -62,6 +62,29 @@ def test_backward_refusals(kw, status):
     assert tp.tp_attention_scored_backward(**a) == status
 
 
+def test_decode_refusals():
+    size = tp.tp_attention_decode_workspace_size(3, 100, 2, 8, 4, 128)
+    assert size > 0 and tp.tp_attention_decode_workspace_size(3, 0, 2, 8, 4, 128) == 0
+
+    def call(**kw):
+        a = dict(Q=B[0], K_new=B[1], V_new=B[2], K_cache=B[3], V_cache=B[4], lengths=B[5], O=B[6], LSE=B[7],
+                 workspace=B[8], workspace_bytes=size, B=3, capacity=100, p=2, n_heads=8, n_kv_heads=4,
+                 head_dim=128, score=None, stream=0, check=False)
+        a.update(kw)
+        return tp.tp_attention_decode(**a)
+
+    for kw, status in [(dict(B=-1), 1), (dict(B=2 ** 31), 4), (dict(p=0), 1), (dict(n_heads=6, n_kv_heads=4), 1),
+                       (dict(n_heads=7), 2), (dict(head_dim=96), 4), (dict(capacity=0), 1), (dict(capacity=2 ** 31), 4),
+                       (dict(Q=None), 1), (dict(K_new=None), 1), (dict(V_new=None), 1), (dict(K_cache=None), 1),
+                       (dict(V_cache=B[4] + 8), 3), (dict(lengths=None), 1), (dict(lengths=B[5] + 1), 3),
+                       (dict(LSE=B[7] + 2), 3), (dict(workspace=None), 7), (dict(workspace_bytes=size - 1), 7),
+                       (dict(workspace=B[8] + 128), 3), (dict(V_cache=B[3]), 1), (dict(O=B[0]), 1),
+                       (dict(K_new=B[3] + 256), 1), (dict(score=tp.score_params(mask=B[9])), 4),
+                       (dict(score=tp.score_params(softcap=-1.0)), 1)]:
+        assert call(**kw) == status, kw
+    assert call(B=0, Q=None, K_cache=None) == 0
+
+
 def test_nothing_to_do():
     n0 = tp.tp_kernel_launch_count()
     assert tp.tp_attention_scored(None, None, None, None, None, 0, 1, 1, 1, 128, stream=0, check=False) == 0

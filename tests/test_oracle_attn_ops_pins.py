@@ -106,3 +106,13 @@ def test_scored_gradients_against_differences(cap, slope):
             y[n][idx] -= 2 * h
             down = (A.scored_head(*y, seen, 0.7, cap, slope)[0] * do).sum()
             assert abs((up - down) / (2 * h) - grads[n][idx]) < 1e-7
+
+
+def test_scored_row_is_the_last_row_of_the_causal_head():
+    rng = np.random.default_rng(5)
+    q, k, v = (rng.standard_normal((7, 4)) for _ in range(3))
+    seen, _ = A.visible(7, True)
+    o, lse = A.scored_head(q, k, v, seen, 0.4, 2.0, 0.3)
+    row, l1 = A.scored_row(q[6], k, v, 0.4, 2.0, 0.3)
+    assert np.allclose(row, o[6], atol=1e-13) and abs(l1 - lse[6]) < 1e-12
+    assert A.scored_row(q[0], k[:0], v[:0], 0.4)[1] == -np.inf
