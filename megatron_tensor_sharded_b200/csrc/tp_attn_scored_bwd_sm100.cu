@@ -22,10 +22,9 @@
 // then owns a key row, and P^T and dS^T, left in TMEM as bf16, are the A
 // operands of dV += P^T dO and dK += dS^T Q, whose B operands are the tiles
 // that S^T and dP^T read: no operand is transposed or written to shared
-// memory.  dq likewise: dQ += dS K.  The eight arithmetic warps split a tile
-// by column halves; each half's bf16 result goes over its own half's scores
-// (columns 0..31 and 64..95 of the buffer), so the halves never wait for one
-// another.  The tensor core runs dV and the next S^T while the warps form
+// memory.  dq likewise: dQ += dS K.  The sixteen arithmetic warps split a tile
+// by column quarters; each quarter's bf16 result goes over the first half of
+// its own scores, so the quarters never wait for one another.  The tensor core runs dV and the next S^T while the warps form
 // dS^T, and dK and the next dP^T while they form P^T.
 //
 // Masks, and rows that hold infinities or NaN outside what is seen, as in the
@@ -57,17 +56,22 @@ constexpr int TILE_BYTES = 128 * 128 * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;
 constexpr int VEC_BYTES = 4 * BT * 4;        // per slot: -LSE log2 e, D, first and last + 1 key in sight
 constexpr int SMEM_BYTES = 1024 + 2 * TILE_BYTES + NST * 2 * TILE_BYTES + NST * VEC_BYTES + 512;   // + barriers, flags
-constexpr int NUM_THREADS = 384;
+constexpr int NUM_THREADS = 640;
+constexpr int ARITH = 512;                   // threads that form P and dS
 constexpr uint32_t IDESC_KK = idesc_bf16_f32(BT, BT, 0, 0);   // both operands along head_dim
 constexpr uint32_t IDESC_KN = idesc_bf16_f32(BT, DH, 0, 1);   // A in TMEM, B rows x head_dim
-constexpr int POLY_PAIRS = 2;
+// Of every eight pairs of probabilities, those whose 2^x runs on the FMA pipe:
+// none with the cap, whose own arithmetic there (11 clocks of a scheduler an
+// element against the MUFU unit's 8) is the longer already.
+template <bool CAP>
+constexpr int kPolyPairs = CAP ? 0 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
   int32_t T, p, hq, hkv, group, tiles, num_units, causal;
   MaskPlan mask;
   ScoreConsts s;
-  float inv_cap_log2;
+  float neg_inv_cap2;       // -(cap log2 e)^-2: 1 - tanh^2 = 1 + z^2 times it
   const float* slopes;
   const float* LSE;
   const float* delta;
@@ -90,12 +94,12 @@ __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b) {
                kk > 0 ? 1u : 0u);
   }
 }
-// D (+)= A B with A (bf16, the halves at columns 0 and 64) in TMEM and B's
-// 128 rows the contraction.
+// D (+)= A B with A (bf16, each column quarter at its 32 columns' start) in
+// TMEM and B's 128 rows the contraction.
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool add) {
 #pragma unroll
   for (int kk = 0; kk < BT / 16; ++kk)
-    tc_mma_f16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8,
+    tc_mma_f16_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8,
                   smem_desc_sw128(b + kk * 16 * 128, HALF_BYTES, 1024), IDESC_KN,
                   (add || kk > 0) ? 1u : 0u);
 }
@@ -106,42 +110,50 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     tma_load_3d(dst + c * HALF_BYTES, map, bar, head * DH + c * 64, row, shard);
 }
 
-// 32 raw products -> P (kept in w, times the cap's derivative) and bf16 pairs
-// of P in pk.  nl(e): -LSE log2 e of column e; seen(e): whether the pair counts.
-template <bool CAP, bool BIAS, bool MASK, typename NegLse, typename Seen>
-__device__ __forceinline__ void prob_chunk(uint32_t* v, float* w, uint32_t (&pk)[16],
+// 32 raw products -> P as bf16 pairs in pk and w = P (1 - tanh^2).  nl(e):
+// -LSE log2 e of columns e and e + 1; seen(e): whether the pair counts.
+template <bool CAP, bool BIAS, typename NegLse, typename Seen>
+__device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], uint32_t (&pk)[16],
                                            const BwdParams& P, float slope2, float dist0, int side,
-                                           NegLse nl, Seen seen) {
-  if (CAP) cap_chunk(v, P.s);
+                                           bool cut, NegLse nl, Seen seen) {
   if (CAP) {
-    const uint64_t ic = f2_pack(P.inv_cap_log2, P.inv_cap_log2), one = f2_pack(1.0f, 1.0f);
-    const uint64_t neg = f2_pack(-1.0f, -1.0f);
+    cap_chunk(v, P.s);
+    const uint64_t ic = f2_pack(P.neg_inv_cap2, P.neg_inv_cap2), one = f2_pack(1.0f, 1.0f);
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {   // 1 - tanh^2
-      const uint64_t t = f2_mul(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ic);
-      f2_unpack(f2_fma(f2_mul(t, neg), t, one), w[e], w[e + 1]);
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t z = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+      f2_unpack(f2_fma(f2_mul(z, z), ic, one), w[e], w[e + 1]);
     }
   }
   if (BIAS) bias_chunk<!CAP>(v, P.s.scale_log2, slope2, dist0, side);
-  const float sc = CAP || BIAS ? 1.0f : P.s.scale_log2;
-  const uint64_t sc2 = f2_pack(sc, sc);
+  const uint64_t sc2 = f2_pack(P.s.scale_log2, P.s.scale_log2);
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    const uint64_t x =
-        f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nl(e));
+    uint64_t x = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    x = CAP || BIAS ? f2_add(x, nl(e)) : f2_fma(x, sc2, nl(e));
     float a, b;
-    if ((e / 2) % 8 < POLY_PAIRS) {
-      f2_unpack(exp2_poly2_nan(x), a, b);
+    if ((e / 2) % 8 < kPolyPairs<CAP>) {
+      f2_unpack(exp2_poly5<true>(x), a, b);
     } else {
       float x0, x1;
       f2_unpack(x, x0, x1);
       a = ex2(x0);
       b = ex2(x1);
     }
-    if (MASK) {
-      if (!seen(e)) a = 0.0f;
-      if (!seen(e + 1)) b = 0.0f;
-    }
+    v[e] = __float_as_uint(a);
+    v[e + 1] = __float_as_uint(b);
+  }
+  if (cut) {   // (the cap's derivative of what is not seen may be NaN)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!seen(e)) {
+        v[e] = 0;
+        if (CAP) w[e] = 0.0f;
+      }
+  }
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float a = __uint_as_float(v[e]), b = __uint_as_float(v[e + 1]);
     pk[e / 2] = pack2(a, b);
     if (CAP) {
       f2_unpack(f2_mul(f2_pack(a, b), f2_pack(w[e], w[e + 1])), w[e], w[e + 1]);
@@ -152,40 +164,42 @@ __device__ __forceinline__ void prob_chunk(uint32_t* v, float* w, uint32_t (&pk)
   }
 }
 
-// 32 products dP -> dS = w (dP - D) as bf16 pairs; nd(e): -D of column e.
-template <bool MASK, typename NegDelta, typename Seen>
-__device__ __forceinline__ void grad_chunk(const uint32_t* v, const float* w, uint32_t (&pk)[16],
-                                           NegDelta nd, Seen seen) {
+// 32 products dP -> dS = w (dP - D) as bf16 pairs; nd(e): -D of columns e, e + 1.
+template <typename NegDelta, typename Seen>
+__device__ __forceinline__ void grad_chunk(uint32_t (&v)[32], const float (&w)[32],
+                                           uint32_t (&pk)[16], bool cut, NegDelta nd, Seen seen) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     const uint64_t x = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), nd(e));
     float a, b;
     f2_unpack(f2_mul(x, f2_pack(w[e], w[e + 1])), a, b);
-    if (MASK) {   // 0 * NaN from what is not seen
-      if (!seen(e)) a = 0.0f;
-      if (!seen(e + 1)) b = 0.0f;
-    }
-    pk[e / 2] = pack2(a, b);
+    v[e] = __float_as_uint(a);
+    v[e + 1] = __float_as_uint(b);
   }
+  if (cut) {   // 0 * NaN from what is not seen
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!seen(e)) v[e] = 0;
+  }
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    pk[e / 2] = pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
 }
 
-// 64 accumulator columns of the thread's row, times f, to bf16 at dst.
-__device__ __forceinline__ void store_half_row(uint32_t taddr, float f, bool store,
+// 32 accumulator columns of the thread's row, times f, to bf16 at dst.
+__device__ __forceinline__ void store_part_row(uint32_t taddr, float f, bool store,
                                                __nv_bfloat16* dst) {
+  uint32_t v[32];
+  tmem_ld_32x32b_x32(taddr, v);
+  tmem_ld_wait();
+  if (!store) return;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(taddr + c * 32, v);
-    tmem_ld_wait();
-    if (!store) continue;
+  for (int g = 0; g < 4; ++g) {
+    uint32_t o[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = pack2(__uint_as_float(v[g * 8 + 2 * i]) * f, __uint_as_float(v[g * 8 + 2 * i + 1]) * f);
-      *reinterpret_cast<uint4*>(dst + c * 32 + g * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+    for (int i = 0; i < 4; ++i)
+      o[i] = pack2(__uint_as_float(v[g * 8 + 2 * i]) * f, __uint_as_float(v[g * 8 + 2 * i + 1]) * f);
+    *reinterpret_cast<uint4*>(dst + g * 8) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -283,8 +297,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* const cut_flag = tmem_slot + 2;   // [NST]: the step's tile is cut by a mask
   volatile uint32_t* const bad = tmem_slot + 4;        // [NST][4]: its rows of dO or Q that are not finite
-  // [3][4]: keys that see one, by unit number mod 3 (set by either column
-  // half's thread of the key, read by both at the unit's end; cleared two
+  // [3][4]: keys that see one, by unit number mod 3 (set by any column
+  // quarter's thread of the key, read by all at the unit's end; cleared two
   // units ahead, when the last reader of the slot has moved on)
   uint32_t* const hit = tmem_slot + 4 + NST * 4;
 
@@ -299,10 +313,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 256);
-    mbar_init(ds_full, 256);
+    mbar_init(p_full, ARITH);
+    mbar_init(ds_full, ARITH);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 256);
+    mbar_init(acc_empty, ARITH);
     mbar_init(drain, 1);
     *abort_flag = 0;
     for (int i = 0; i < 12; ++i) hit[i] = 0;
@@ -329,9 +343,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // 168 registers a thread at launch: 128 x 96 + 256 x 200 <= 384 x 168
+  // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
-    regs_shrink<96>();
+    regs_shrink<64>();
     if (warp == 0) {
       if (lane == 0) {
         // ---------------------------------------------------------- producer
@@ -492,11 +506,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else {
-    regs_grow<200>();
+    regs_grow<104>();
     // -------------------------------------------- P^T, dS^T and the outputs
-    const int half = (warp - 4) / 4;         // columns [64 half, 64 half + 64)
+    const int part = (warp - 4) / 4;         // columns [32 part, 32 part + 32)
     const int quad = warp & 3;
-    const uint32_t off = (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+    const uint32_t off = (static_cast<uint32_t>(quad * 32) << 16) + part * 32;
     uint32_t n = 0, nu = 0;
     bool ok = true;
     int32_t r = 0;
@@ -515,38 +529,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const bool cut = cut_flag[st] != 0;
-          const uint32_t vl = vec(st, 0) + half * 256, vd = vec(st, 1) + half * 256;
-          const uint32_t va = vec(st, 2) + half * 256, vb = vec(st, 3) + half * 256;
-          const float dist0 = static_cast<float>(i * BT + half * 64 - key);
+          const uint32_t vl = vec(st, 0) + part * 128, vd = vec(st, 1) + part * 128;
+          const uint32_t va = vec(st, 2) + part * 128, vb = vec(st, 3) + part * 128;
+          const float dist0 = static_cast<float>(i * BT + part * 32 - key);
           const int side = i * BT >= x.kb * BT + BT - 1 ? 1 : i * BT + BT - 1 <= x.kb * BT ? -1 : 0;
-          float w[64];
-          uint32_t seen[2] = {0xffffffffu, 0xffffffffu};   // columns that see this key
+          float w[32];
+          uint32_t seen = 0xffffffffu;   // columns that see this key
           if (cut) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              seen[c] = 0;
-              for (int e = 0; e < 32; ++e) {
-                const int32_t a = __float_as_int(lds(va + (c * 32 + e) * 4));
-                const int32_t b = __float_as_int(lds(vb + (c * 32 + e) * 4));
-                seen[c] |= static_cast<uint32_t>(key >= a && key < b) << e;
-              }
-              if (seen[c] & bad[st * 4 + half * 2 + c])
-                atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
+            seen = 0;
+            for (int e = 0; e < 32; ++e) {
+              const int32_t a = __float_as_int(lds(va + e * 4)), b = __float_as_int(lds(vb + e * 4));
+              seen |= static_cast<uint32_t>(key >= a && key < b) << e;
             }
+            if (seen & bad[st * 4 + part]) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
           }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[32], pk[16];
-            tmem_ld_32x32b_x32(tS + off + c * 32, v);
-            tmem_ld_wait();
-            auto nl = [&](int e) { return lds2(vl + (c * 32 + e) * 4); };
-            auto sees = [&](int e) { return (seen[c] >> e) & 1u; };
-            if (cut)
-              prob_chunk<CAP, BIAS, true>(v, w + c * 32, pk, P, slope2, dist0 + c * 32.0f, side, nl, sees);
-            else
-              prob_chunk<CAP, BIAS, false>(v, w + c * 32, pk, P, slope2, dist0 + c * 32.0f, side, nl, sees);
-            tmem_st_32x32b_x16(tS + off + c * 16, pk);
-          }
+          uint32_t v[32], pk[16];
+          auto sees = [&](int e) { return ((seen >> e) & 1u) != 0; };
+          tmem_ld_32x32b_x32(tS + off, v);
+          tmem_ld_wait();
+          prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut,
+                                [&](int e) { return lds2(vl + e * 4); }, sees);
+          tmem_st_32x32b_x16(tS + off, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(p_full);
@@ -554,19 +557,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[32], pk[16];
-            tmem_ld_32x32b_x32(tdP + off + c * 32, v);
-            tmem_ld_wait();
-            auto nd = [&](int e) { return lds2(vd + (c * 32 + e) * 4); };
-            auto sees = [&](int e) { return (seen[c] >> e) & 1u; };
-            if (cut)
-              grad_chunk<true>(v, w + c * 32, pk, nd, sees);
-            else
-              grad_chunk<false>(v, w + c * 32, pk, nd, sees);
-            tmem_st_32x32b_x16(tdP + off + c * 16, pk);
-          }
+          tmem_ld_32x32b_x32(tdP + off, v);
+          tmem_ld_wait();
+          grad_chunk(v, w, pk, cut, [&](int e) { return lds2(vd + e * 4); }, sees);
+          tmem_st_32x32b_x16(tdP + off, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(ds_full);
@@ -580,12 +574,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // keys of no document stay as they were
       const bool store = key < P.T && row_span(P.mask, key, P.T, P.causal).y >= 0;
       const int64_t row =
-          ((static_cast<int64_t>(x.shard) * P.T + key) * P.hkv + x.kvh) * DH + half * 64;
+          ((static_cast<int64_t>(x.shard) * P.T + key) * P.hkv + x.kvh) * DH + part * 32;
       const uint32_t hits = *const_cast<volatile uint32_t*>(&hit[(nu % 3) * 4 + quad]);
       const float f = (hits >> lane) & 1u ? NAN : 1.0f;
-      if (half == 0 && lane == 0) hit[((nu + 2) % 3) * 4 + quad] = 0;
-      store_half_row(tdV + off, f, store, P.dV + row);
-      store_half_row(tdK + off, f * P.s.scale, store, P.dK + row);
+      if (part == 0 && lane == 0) hit[((nu + 2) % 3) * 4 + quad] = 0;
+      store_part_row(tdV + off, f, store, P.dV + row);
+      store_part_row(tdK + off, f * P.s.scale, store, P.dK + row);
       tc_fence_before();
       mbar_arrive(acc_empty);
       ++nu;
@@ -653,10 +647,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(k_seen(s), 64);
     }
     mbar_init(dp_full, 1);
-    mbar_init(dp_free, 256);
-    mbar_init(ds_full, 256);
+    mbar_init(dp_free, ARITH);
+    mbar_init(ds_full, ARITH);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 256);
+    mbar_init(acc_empty, ARITH);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -678,9 +672,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const uint32_t tdP = tm + 256, tdQ = tm + 384;   // S buffers at 0 and 128
 
-  // 168 registers a thread at launch: 128 x 96 + 256 x 200 <= 384 x 168
+  // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
-    regs_shrink<96>();
+    regs_shrink<64>();
     if (warp == 0) {
       if (lane == 0) {
         // ---------------------------------------------------------- producer
@@ -811,11 +805,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else {
-    regs_grow<200>();
+    regs_grow<104>();
     // ------------------------------------------------ P, dS and the output
-    const int half = (warp - 4) / 4;
+    const int part = (warp - 4) / 4;         // columns [32 part, 32 part + 32)
     const int quad = warp & 3;
-    const uint32_t off = (static_cast<uint32_t>(quad * 32) << 16) + half * 64;
+    const uint32_t off = (static_cast<uint32_t>(quad * 32) << 16) + part * 32;
     uint32_t n = 0, nu = 0, looked = 0;
     bool ok = true;
     int32_t r = 0;
@@ -842,44 +836,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int32_t key0 = j * BT + half * 64, rl = span.x - key0, rh = span.y - key0;
+        const int32_t key0 = j * BT + part * 32, rl = span.x - key0, rh = span.y - key0;
         const float dist0 = static_cast<float>(key0 - q);
         const int side = j * BT + BT - 1 <= q0 ? -1 : j * BT >= q0 + BT - 1 ? 1 : 0;
-        float w[64];
-        auto nl = [&](int) { return nlse; };
-        auto nd = [&](int) { return ndl; };
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[32], pk[16];
-          tmem_ld_32x32b_x32(tS + c * 32, v);
-          tmem_ld_wait();
-          auto sees = [&](int e) { return c * 32 + e >= rl && c * 32 + e < rh; };
-          if (cut)
-            prob_chunk<CAP, BIAS, true>(v, w + c * 32, pk, P, slope2, dist0 + c * 32.0f, side, nl, sees);
-          else
-            prob_chunk<CAP, BIAS, false>(v, w + c * 32, pk, P, slope2, dist0 + c * 32.0f, side, nl, sees);
-        }
+        float w[32];
+        uint32_t v[32], pk[16];
+        auto sees = [&](int e) { return e >= rl && e < rh; };
+        tmem_ld_32x32b_x32(tS, v);
+        tmem_ld_wait();
+        // (P itself is not stored: dQ needs dS alone)
+        prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut, [&](int) { return nlse; }, sees);
         ok = wait_bounded(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[64];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          tmem_ld_32x32b_x32(tdP + off + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+        tmem_ld_32x32b_x32(tdP + off, v);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(dp_free);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
-          auto sees = [&](int e) { return c * 32 + e >= rl && c * 32 + e < rh; };
-          if (cut)
-            grad_chunk<true>(v + c * 32, w + c * 32, pk, nd, sees);
-          else
-            grad_chunk<false>(v + c * 32, w + c * 32, pk, nd, sees);
-          tmem_st_32x32b_x16(tS + c * 16, pk);
-        }
+        grad_chunk(v, w, pk, cut, [&](int) { return ndl; }, sees);
+        tmem_st_32x32b_x16(tS, pk);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(ds_full);
@@ -889,8 +865,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      store_half_row(tdQ + off, P.s.scale, live,
-                     P.dQ + ((static_cast<int64_t>(x.shard) * P.T + q) * P.hq + x.head) * DH + half * 64);
+      store_part_row(tdQ + off, P.s.scale, live,
+                     P.dQ + ((static_cast<int64_t>(x.shard) * P.T + q) * P.hq + x.head) * DH + part * 32);
       tc_fence_before();
       mbar_arrive(acc_empty);
       ++nu;
@@ -976,7 +952,7 @@ tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a) {
   prm.causal = a.causal ? 1 : 0;
   prm.mask = mask_plan(a.mask, a.T);
   prm.s = score_consts(a.scale, a.cap);
-  prm.inv_cap_log2 = a.cap > 0.0f ? 1.0f / prm.s.cap_log2 : 0.0f;
+  prm.neg_inv_cap2 = a.cap > 0.0f ? -1.0f / (prm.s.cap_log2 * prm.s.cap_log2) : 0.0f;
   prm.slopes = a.slopes;
   prm.LSE = a.LSE;
   prm.delta = a.delta;

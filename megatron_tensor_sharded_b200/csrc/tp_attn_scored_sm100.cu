@@ -60,14 +60,14 @@ constexpr int NQT = 2;                       // query tiles per unit
 constexpr int NST = 2;                       // K/V ring slots
 constexpr int TILE_BYTES = 128 * 128 * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;
-constexpr int SMEM_BYTES = 1024 + NQT * TILE_BYTES + NST * 2 * TILE_BYTES + 512;
-constexpr int NUM_THREADS = 384;
+constexpr int XCH_BYTES = NQT * 2 * 2 * BQ * 4;   // [tile][parity][column half][row]
+constexpr int SMEM_BYTES = 1024 + NQT * TILE_BYTES + NST * 2 * TILE_BYTES + XCH_BYTES + 512;
+constexpr int NUM_THREADS = 640;
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BQ, BKV, 0, 0);
 constexpr uint32_t IDESC_O = idesc_bf16_f32(BQ, DH, 0, 1);
 constexpr uint32_t O_COL0 = NQT * BKV, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float kBoundLog2 = 80.0f;          // |z| in log2 that needs no running maximum
-constexpr int POLY_PAIRS = 2;                // of every 8 probability pairs, by the polynomial exp2
 
 enum { kPlain = 0, kBias = 1, kCap = 2, kCapAny = 3 };   // kCap: no bias, bounded
 
@@ -124,16 +124,26 @@ __device__ __forceinline__ int32_t unit_of(int32_t r) {
   return r * g + ((r & 1) ? g - 1 - b : b);
 }
 
-// Probabilities of 32 scores (log2 units, the maximum taken off): bf16 pairs
-// into pk, fp32 sums into sum2.
-__device__ __forceinline__ void exp_chunk(const uint32_t* v, uint64_t sc2, uint64_t nm2,
+// Of every eight pairs of probabilities, those whose 2^x runs as a polynomial
+// on the FMA pipe, so that it and the MUFU unit (16 a clock and SM) are busy
+// for about as long: an element costs the FMA pipe 6 clocks of a scheduler
+// with the cap and 2 to 3 without, 9 more where 2^x is there too, and the MUFU
+// unit 8 where it is not.
+template <int MODE>
+constexpr int kPolyPairs = MODE == kCap || MODE == kCapAny ? 1 : 2;
+
+// Probabilities of 32 scores: bf16 pairs into pk, fp32 sums into sum2.
+// SCALE: x = v * sc + off, else v holds x itself.
+template <int POLY, bool SCALE>
+__device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint64_t sc2, uint64_t off2,
                                           uint64_t (&sum2)[2], uint32_t (&pk)[16]) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    const uint64_t xa = f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nm2);
+    uint64_t xa = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    if (SCALE) xa = f2_fma(xa, sc2, off2);
     float a0, a1;
-    if ((e / 2) % 8 < POLY_PAIRS) {
-      f2_unpack(exp2_poly2(xa), a0, a1);
+    if ((e / 2) % 8 < POLY) {
+      f2_unpack(exp2_poly5<false>(xa), a0, a1);
     } else {
       float x0, x1;
       f2_unpack(xa, x0, x1);
@@ -145,79 +155,22 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* v, uint64_t sc2, uint6
   }
 }
 
-// One softmax step of a thread's row over the 128 scores in TMEM columns
-// [tS, tS + 128); the probabilities go back as bf16 pairs into [tS, tS + 64).
-// [rl, rh): the row's visible columns (MASK).  Returns the probabilities' sum.
-template <int MODE, bool MASK>
-__device__ __forceinline__ float softmax_block(uint32_t tS, const ScoreConsts& S, float& m,
-                                               float& alpha, bool& grow, int32_t rl,
-                                               int32_t rh, float slope2, float dist0, int side) {
-  bool lost = false;   // a visible score that is NaN (the polynomial exp2 does not carry it)
-  uint64_t sum2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
-  const uint64_t one2 = f2_pack(1.0f, 1.0f);
-  alpha = 1.0f;
-  grow = false;
-  if (MODE == kCap) {
-    // bounded scores, no maximum: chunk by chunk, the next chunk's scores on
-    // their way while this one is worked on
-    uint32_t v[2][32];
-    tmem_ld_32x32b_x32(tS, v[0]);
+// 32 raw products -> scores in log2 units (kPlain: still unscaled), -inf where
+// the row does not see the key.  lost: a visible score is NaN (kCap has no
+// maximum that would carry it).
+template <int MODE>
+__device__ __forceinline__ void score_chunk(uint32_t (&v)[32], const ScoreConsts& S, float slope2,
+                                            float dist0, int side, bool whole, int32_t rl,
+                                            int32_t rh, bool& lost) {
+  bool slow = false;
+  if (MODE == kCap || MODE == kCapAny) slow = cap_chunk(v, S);
+  if (MODE == kBias || MODE == kCapAny)
+    bias_chunk<MODE == kBias>(v, S.scale_log2, slope2, dist0, side);
+  if (!whole) mask_chunk(v, rl, rh);
+  if (MODE == kCap && slow) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t* const w = v[c & 1];
-      tmem_ld_wait();
-      if (c < 3) tmem_ld_32x32b_x32(tS + (c + 1) * 32, v[(c + 1) & 1]);
-      const bool slow = cap_chunk(w, S);
-      if (MASK) mask_chunk(w, rl - c * 32, rh - c * 32);
-      if (slow) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) lost |= __uint_as_float(w[e]) != __uint_as_float(w[e]);
-      }
-      uint32_t pk[16];
-      exp_chunk(w, one2, f2_pack(0.0f, 0.0f), sum2, pk);
-      tmem_st_32x32b_x16(tS + c * 16, pk);
-    }
-  } else {
-    uint32_t v[128];
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      tmem_ld_32x32b_x32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-    tmem_ld_wait();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (MODE == kCapAny) cap_chunk(&v[c * 32], S);
-      if (MODE != kPlain)
-        bias_chunk<MODE == kBias>(&v[c * 32], S.scale_log2, slope2,
-                                  dist0 + static_cast<float>(c * 32), side);
-      if (MASK) mask_chunk(&v[c * 32], rl - c * 32, rh - c * 32);
-    }
-    float acc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int e = 0; e < 128; e += 8) {
-      const int a = (e / 8) & 3;
-#pragma unroll
-      for (int q = 0; q < 8; q += 2)
-        acc[a] = max3_nan(acc[a], __uint_as_float(v[e + q]), __uint_as_float(v[e + q + 1]));
-    }
-    float m_cand = max3_nan(max3_nan(acc[0], acc[1], acc[2]), acc[3], acc[3]);
-    if (MODE == kPlain) m_cand *= S.scale_log2;
-    grow = !(m_cand <= m + RESCALE_LOG2);   // NaN too: it then stays in the sum
-    alpha = grow ? ex2(m - m_cand) : 1.0f;
-    if (grow) m = m_cand;
-    const float off = m == -INFINITY ? 0.0f : -m;   // nothing seen so far
-    const uint64_t sc2 = MODE == kPlain ? f2_pack(S.scale_log2, S.scale_log2) : one2;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t pk[16];
-      exp_chunk(&v[c * 32], sc2, f2_pack(off, off), sum2, pk);
-      tmem_st_32x32b_x16(tS + c * 16, pk);
-    }
+    for (int e = 0; e < 32; ++e) lost |= __uint_as_float(v[e]) != __uint_as_float(v[e]);
   }
-  tmem_st_wait();
-  float s0, s1, s2, s3;
-  f2_unpack(sum2[0], s0, s1);
-  f2_unpack(sum2[1], s2, s3);
-  return lost ? NAN : (s0 + s1) + (s2 + s3);
 }
 
 template <int MODE>
@@ -232,7 +185,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto sQ = [&](uint32_t t) { return base + t * TILE_BYTES; };
   auto sK = [&](uint32_t st) { return base + NQT * TILE_BYTES + st * 2 * TILE_BYTES; };
   auto sV = [&](uint32_t st) { return sK(st) + TILE_BYTES; };
-  uint8_t* const ctrl = smem_raw + (base - raw) + NQT * TILE_BYTES + NST * 2 * TILE_BYTES;
+  constexpr int RING_END = NQT * TILE_BYTES + NST * 2 * TILE_BYTES;
+  volatile float* const xch = reinterpret_cast<volatile float*>(smem_raw + (base - raw) + RING_END);
+  uint8_t* const ctrl = smem_raw + (base - raw) + RING_END + XCH_BYTES;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl);
   const uint32_t q_full = smem_u32(&bars[0]), q_empty = smem_u32(&bars[1]);
   auto kv_full = [&](uint32_t s) { return smem_u32(&bars[2 + s]); };
@@ -242,8 +197,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto o_full = [&](uint32_t t) { return smem_u32(&bars[2 + 2 * NST + 2 * NQT + t]); };
   auto o_empty = [&](uint32_t t) { return smem_u32(&bars[2 + 2 * NST + 3 * NQT + t]); };
   auto v_seen = [&](uint32_t i) { return smem_u32(&bars[2 + 2 * NST + 4 * NQT + i]); };
-  const uint32_t drain = smem_u32(&bars[4 + 2 * NST + 4 * NQT]);
-  constexpr int NBARS = 5 + 2 * NST + 4 * NQT;
+  auto x_full = [&](uint32_t t) { return smem_u32(&bars[4 + 2 * NST + 4 * NQT + t]); };
+  const uint32_t drain = smem_u32(&bars[6 + 2 * NST + 4 * NQT]);
+  constexpr int NBARS = 7 + 2 * NST + 4 * NQT;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* const bad = tmem_slot + 2;   // [2][4]: keys of a looked-at block whose V is not finite
@@ -258,9 +214,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int t = 0; t < NQT; ++t) {
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 128);
+      mbar_init(p_full(t), 256);
       mbar_init(o_full(t), 1);
-      mbar_init(o_empty(t), 128);
+      mbar_init(o_empty(t), 256);
+      mbar_init(x_full(t), 256);
       mbar_init(v_seen(t), 64);
     }
     mbar_init(drain, 1);
@@ -283,9 +240,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   pdl_wait();
   pdl_launch_dependents();
-  // 168 registers a thread at launch: 128 x 96 + 256 x 200 <= 384 x 168
+  // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
-    regs_shrink<96>();
+    regs_shrink<64>();
     if (warp == 0) {
       if (lane == 0) {
         // ------------------------------------------------------------ producer
@@ -401,8 +358,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   #pragma unroll
                 for (int kk = 0; kk < BKV / 16; ++kk) {
                   const uint64_t bdesc = smem_desc_sw128(sV(vst) + kk * 16 * 128, HALF_BYTES, 1024);
-                  tc_mma_f16_ts(tmem_base + O_COL0 + t * DH, tmem_base + t * BKV + kk * 8, bdesc,
-                                IDESC_O, (j > x.t[t].jb || kk > 0) ? 1u : 0u);
+                  tc_mma_f16_ts(tmem_base + O_COL0 + t * DH,
+                                tmem_base + t * BKV + (kk >> 2) * 64 + (kk & 3) * 8, bdesc, IDESC_O,
+                                (j > x.t[t].jb || kk > 0) ? 1u : 0u);
                 }
                 ++pv[t];
                 if (t == NQT - 1 || !a1) tc_commit(kv_empty(vst));   // the block's last reader
@@ -460,27 +418,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else {
-    regs_grow<200>();
+    regs_grow<104>();
     // ------------------------------------------------------- softmax / output
-    const int t = (warp - 4) / 4;
+    // thread = row and column half: scores [64 half, 64 half + 64) of a block,
+    // and those columns of O
+    const int t = (warp - 4) / 8;
+    const int half = ((warp - 4) / 4) & 1;
     const int quad = warp & 3;
+    const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem_base + lane_off + t * BKV;
-    const uint32_t tO = tmem_base + lane_off + O_COL0 + t * DH;
-    uint32_t sc = 0, uc = 0, looked = 0;
+    const uint32_t tS = tmem_base + lane_off + t * BKV + half * 64;
+    const uint32_t tO = tmem_base + lane_off + O_COL0 + t * DH + half * 64;
+    constexpr bool HAS_MAX = MODE != kCap;
+    const ScoreConsts& S = P.s;
+    uint32_t sc = 0, uc = 0, looked = 0, xc = 0;
     bool ok = true;
+    // hands v to the row's other half and takes its
+    auto swap_halves = [&](float v, float* other) {
+      xch[((t * 2 + (xc & 1)) * 2 + half) * BQ + row] = v;
+      mbar_arrive(x_full(t));
+      const bool got = wait_bounded(x_full(t), xc & 1, abort_flag, P.wait, kErrWaitAttn);
+      *other = xch[((t * 2 + (xc & 1)) * 2 + (half ^ 1)) * BQ + row];
+      ++xc;
+      return __all_sync(0xffffffffu, got) != 0;
+    };
     int32_t r = 0;
     for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
       const Unit x = decode_unit(P, u);
       const TileSpan mine = x.span(t);
       const int32_t q0 = (x.qb0 + t) * BQ;
-      const int32_t q = q0 + quad * 32 + lane;
+      const int32_t q = q0 + row;
       const int2 seen = row_span(P.mask, q, P.T, P.causal);
       float slope2 = 0.0f;
       if (MODE == kBias || MODE == kCapAny)
         slope2 = P.slopes != nullptr ? 1.4426950408889634f * P.slopes[x.shard * P.hq + x.head] : 0.0f;
-      float m = -INFINITY, l = 0.0f;
-      bool poison = false;
+      float m = HAS_MAX ? -INFINITY : 0.0f, l = 0.0f;
+      bool poison = false, lost = false;
       for (int32_t j = x.jmin; j < x.jmax; ++j) {
         const bool cut = x.cut(j);
         if (!x.active(t, j)) {
@@ -488,13 +461,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           continue;
         }
         ok = wait_bounded(s_full(t), sc & 1, abort_flag, P.wait, kErrWaitAttn);
-        const int32_t key0 = j * BKV, rl = seen.x - key0, rh = seen.y - key0;
+        const int32_t key0 = j * BKV + half * 64, rl = seen.x - key0, rh = seen.y - key0;
         if (ok && cut) {
           ok = wait_bounded(v_seen(looked & 1), (looked >> 1) & 1, abort_flag, P.wait, kErrWaitAttn);
           if (ok) {
-            const volatile uint32_t* b = bad + (looked & 1) * 4;
-            if (b[0] | b[1] | b[2] | b[3]) {
-              for (int e = 0; e < BKV; ++e)
+            const volatile uint32_t* b = bad + (looked & 1) * 4 + half * 2;
+            if (b[0] | b[1]) {
+              for (int e = 0; e < 64; ++e)
                 poison |= e >= rl && e < rh && ((b[e >> 5] >> (e & 31)) & 1);
             }
           }
@@ -505,44 +478,92 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         const bool whole = mine.whole(j);
         const float dist0 = static_cast<float>(key0 - q);
-        const int side = key0 + BKV - 1 <= q0 ? -1 : key0 >= q0 + BQ - 1 ? 1 : 0;
-        float alpha;
-        bool grow;
-        const float sum =
-            whole ? softmax_block<MODE, false>(tS, P.s, m, alpha, grow, rl, rh, slope2,
-                                               dist0, side)
-                  : softmax_block<MODE, true>(tS, P.s, m, alpha, grow, rl, rh, slope2,
-                                              dist0, side);
-        if (MODE != kCap && j > mine.jb && __any_sync(0xffffffffu, grow)) {
-          // O += P V of the previous block has completed: it was issued before
-          // this score block, whose commit we waited for
-#pragma unroll
-          for (int c = 0; c < DH / 32; ++c) {
+        const int side = j * BKV + BKV - 1 <= q0 ? -1 : j * BKV >= q0 + BQ - 1 ? 1 : 0;
+        uint64_t sum2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
+        // (loops kept rolled: the instruction cache holds one chunk's code)
+        if (HAS_MAX) {
+          float acc[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
             uint32_t v[32];
-            tmem_ld_32x32b_x32(tO + c * 32, v);
+            tmem_ld_32x32b_x32(tS + c * 32, v);
             tmem_ld_wait();
+            score_chunk<MODE>(v, S, slope2, dist0 + c * 32.0f, side, whole, rl - c * 32,
+                              rh - c * 32, lost);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st_32x32b_x32(tO + c * 32, v);
+            for (int e = 0; e < 32; e += 4) {
+              acc[0] = max3_nan(acc[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              acc[1] = max3_nan(acc[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
+            if (MODE != kPlain) tmem_st_32x32b_x32(tS + c * 32, v);
           }
-          tmem_st_wait();
+          if (MODE != kPlain) tmem_st_wait();
+          float m_cand = max3_nan(acc[0], acc[1], acc[1]), other;
+          ok = swap_halves(m_cand, &other);
+          if (!ok) break;
+          m_cand = max3_nan(m_cand, other, other);
+          if (MODE == kPlain) m_cand *= S.scale_log2;
+          const bool grow = !(m_cand <= m + RESCALE_LOG2);   // NaN too: it then stays in the sum
+          const float alpha = grow ? ex2(m - m_cand) : 1.0f;
+          if (grow) m = m_cand;
+          l *= alpha;
+          if (j > mine.jb && __any_sync(0xffffffffu, grow)) {
+            // O += P V of the previous block has completed: it was issued
+            // before this score block, whose commit we waited for
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(tO + c * 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st_32x32b_x32(tO + c * 32, v);
+            }
+          }
         }
-        l = l * alpha + sum;
+        const float off = m == -INFINITY ? 0.0f : -m;   // nothing seen so far
+        const float scale = MODE == kPlain ? S.scale_log2 : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[32], pk[16];
+          tmem_ld_32x32b_x32(tS + c * 32, v);
+          tmem_ld_wait();
+          if (MODE == kPlain && !whole) mask_chunk(v, rl - c * 32, rh - c * 32);
+          if (MODE == kCap)
+            score_chunk<MODE>(v, S, slope2, dist0, side, whole, rl - c * 32, rh - c * 32, lost);
+          exp_chunk<kPolyPairs<MODE>, HAS_MAX>(v, f2_pack(scale, scale), f2_pack(off, off), sum2, pk);
+          tmem_st_32x32b_x16(tS + c * 16, pk);
+        }
+        tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full(t));
+        float s0, s1, s2, s3;
+        f2_unpack(sum2[0], s0, s1);
+        f2_unpack(sum2[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
         ++sc;
       }
       if (!ok) break;
       if (!x.any(t)) continue;
+      // the row's sum over both halves; NaN where a half lost a NaN score, and
+      // a mark where one saw a key whose value is not finite
+      float other;
+      ok = swap_halves(lost ? NAN : l, &other);
+      if (!ok) break;
+      l = lost ? NAN : half == 0 ? l + other : other + l;
+      ok = swap_halves(poison ? 1.0f : 0.0f, &other);
+      if (!ok) break;
+      poison |= other != 0.0f;
       ok = wait_bounded(o_full(t), uc & 1, abort_flag, P.wait, kErrWaitAttn);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const float inv_l = poison ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
       const bool store = q < P.T && seen.y >= 0;   // rows of no document stay as they were
-      __nv_bfloat16* dst = P.O + ((static_cast<int64_t>(x.shard) * P.T + q) * P.hq + x.head) * DH;
-#pragma unroll
-      for (int c = 0; c < DH / 32; ++c) {
+      __nv_bfloat16* dst =
+          P.O + ((static_cast<int64_t>(x.shard) * P.T + q) * P.hq + x.head) * DH + half * 64;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tO + c * 32, v);
         tmem_ld_wait();
@@ -558,9 +579,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if (store && P.LSE != nullptr)
+      if (store && half == 0 && P.LSE != nullptr)
         P.LSE[(static_cast<int64_t>(x.shard) * P.hq + x.head) * P.T + q] =
-            l == 0.0f ? -INFINITY : (MODE == kCap ? 0.0f : 0.6931471805599453f * m) + logf(l);
+            l == 0.0f ? -INFINITY : 0.6931471805599453f * m + logf(l);
       tc_fence_before();
       mbar_arrive(o_empty(t));
       ++uc;
