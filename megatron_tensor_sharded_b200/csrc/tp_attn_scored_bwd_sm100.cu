@@ -24,8 +24,11 @@
 // that S^T and dP^T read: no operand is transposed or written to shared
 // memory.  dq likewise: dQ += dS K.  The sixteen arithmetic warps split a tile
 // by column quarters; each quarter's bf16 result goes over the first half of
-// its own scores, so the quarters never wait for one another.  The tensor core runs dV and the next S^T while the warps form
-// dS^T, and dK and the next dP^T while they form P^T.
+// its own scores, so the quarters never wait for one another.  S^T is free as soon as the warps hold it in registers,
+// since P^T and dS^T both go over dP^T: the next S^T runs while they form P^T,
+// and dV, dK and the next dP^T while they form the next P^T.  (With P^T over
+// S^T, the next S^T waited for dV: 4150 clocks a step against 2048 of
+// products.)
 //
 // Masks, and rows that hold infinities or NaN outside what is seen, as in the
 // forward kernel; here the tiles of Q and dO (dkv) and of K (dq) are looked at.
@@ -51,11 +54,14 @@ namespace {
 
 constexpr int DH = 128;
 constexpr int BT = kAttnTile;                // rows of a tile, keys or queries
-constexpr int NST = 2;                       // ring slots of the walked pair of tiles
+constexpr int NA = 3;                        // ring slots of the tile that the next scores need early (Q; K)
+constexpr int NB = 2;                        // and of its partner (dO; V)
 constexpr int TILE_BYTES = 128 * 128 * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;
-constexpr int VEC_BYTES = 4 * BT * 4;        // per slot: -LSE log2 e, D, first and last + 1 key in sight
-constexpr int SMEM_BYTES = 1024 + 2 * TILE_BYTES + NST * 2 * TILE_BYTES + NST * VEC_BYTES + 512;   // + barriers, flags
+constexpr int VEC_BYTES = 2 * BT * 4;        // per slot: -LSE log2 e, -D
+// 224 KB of tiles: no room to round the start up, it has to be aligned (checked)
+constexpr int TILES_BYTES = (2 + NA + NB) * TILE_BYTES;
+constexpr int SMEM_BYTES = TILES_BYTES + NB * VEC_BYTES + 512;
 constexpr int NUM_THREADS = 640;
 constexpr int ARITH = 512;                   // threads that form P and dS
 constexpr uint32_t IDESC_KK = idesc_bf16_f32(BT, BT, 0, 0);   // both operands along head_dim
@@ -275,45 +281,56 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                          const __grid_constant__ CUtensorMap mapV,
                          const __grid_constant__ CUtensorMap mapdO,
                          const __grid_constant__ BwdParams P) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  if ((base & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(P.wait.err, kErrSmem);
+    return;
+  }
   const uint32_t sK = base, sV = base + TILE_BYTES;
-  auto sQ = [&](uint32_t st) { return base + 2 * TILE_BYTES + st * 2 * TILE_BYTES; };
-  auto sdO = [&](uint32_t st) { return sQ(st) + TILE_BYTES; };
-  constexpr int RING_END = 2 * TILE_BYTES + NST * 2 * TILE_BYTES;
-  auto vec = [&](uint32_t st, int which) { return base + RING_END + st * VEC_BYTES + which * BT * 4; };
-  uint8_t* const ctrl = smem_raw + (base - raw) + RING_END + NST * VEC_BYTES;
+  auto sQ = [&](uint32_t n) { return base + (2 + n % NA) * TILE_BYTES; };
+  auto sdO = [&](uint32_t n) { return base + (2 + NA + n % NB) * TILE_BYTES; };
+  auto vec = [&](uint32_t n, int which) {
+    return base + TILES_BYTES + (n % NB) * VEC_BYTES + which * BT * 4;
+  };
+  uint8_t* const ctrl = smem_raw + TILES_BYTES + NB * VEC_BYTES;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl);
   const uint32_t kv_full = smem_u32(&bars[0]), kv_empty = smem_u32(&bars[1]);
-  auto qd_full = [&](uint32_t s) { return smem_u32(&bars[2 + s]); };
-  auto qd_empty = [&](uint32_t s) { return smem_u32(&bars[4 + s]); };
-  auto vec_full = [&](uint32_t s) { return smem_u32(&bars[6 + s]); };
-  const uint32_t s_full = smem_u32(&bars[8]), dp_full = smem_u32(&bars[9]);
-  const uint32_t p_full = smem_u32(&bars[10]), ds_full = smem_u32(&bars[11]);
-  const uint32_t acc_full = smem_u32(&bars[12]), acc_empty = smem_u32(&bars[13]);
-  const uint32_t drain = smem_u32(&bars[14]);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 15);
+  auto q_full = [&](uint32_t n) { return smem_u32(&bars[2 + n % NA]); };
+  auto q_empty = [&](uint32_t n) { return smem_u32(&bars[5 + n % NA]); };
+  auto do_full = [&](uint32_t n) { return smem_u32(&bars[8 + n % NB]); };
+  auto do_empty = [&](uint32_t n) { return smem_u32(&bars[10 + n % NB]); };
+  auto vec_full = [&](uint32_t n) { return smem_u32(&bars[12 + n % NB]); };
+  const uint32_t s_full = smem_u32(&bars[14]), s_free = smem_u32(&bars[15]);
+  const uint32_t dp_full = smem_u32(&bars[16]), ds_full = smem_u32(&bars[17]);
+  const uint32_t acc_full = smem_u32(&bars[18]), acc_empty = smem_u32(&bars[19]);
+  const uint32_t drain = smem_u32(&bars[20]);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 21);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile uint32_t* const cut_flag = tmem_slot + 2;   // [NST]: the step's tile is cut by a mask
-  volatile uint32_t* const bad = tmem_slot + 4;        // [NST][4]: its rows of dO or Q that are not finite
+  volatile uint32_t* const cut_flag = tmem_slot + 2;   // [NB]: the step's tile is cut by a mask
+  volatile uint32_t* const bad = tmem_slot + 4;        // [NB][4]: its rows of dO or Q that are not finite
   // [3][4]: keys that see one, by unit number mod 3 (set by any column
   // quarter's thread of the key, read by all at the unit's end; cleared two
   // units ahead, when the last reader of the slot has moved on)
-  uint32_t* const hit = tmem_slot + 4 + NST * 4;
+  uint32_t* const hit = tmem_slot + 4 + NB * 4;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(qd_full(s), 1);
-      mbar_init(qd_empty(s), 3);   // the MMA thread's commit, warps 2 and 3
+    // (empty: the MMA thread's commit, warps 2 and 3)
+    for (int s = 0; s < NA; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 3);
+    }
+    for (int s = 0; s < NB; ++s) {
+      mbar_init(do_full(s), 1);
+      mbar_init(do_empty(s), 3);
       mbar_init(vec_full(s), 64);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, ARITH);
+    mbar_init(s_free, ARITH);
     mbar_init(ds_full, ARITH);
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, ARITH);
@@ -349,8 +366,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 0) {
       if (lane == 0) {
         // ---------------------------------------------------------- producer
-        uint32_t nu = 0;
-        int64_t n = 0;
+        uint32_t nu = 0, n = 0, nq = 0;   // nq: loads of Q
         bool ok = true;
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
@@ -364,26 +380,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int32_t g = 0; ok && g < P.group; ++g) {
             const int32_t head = x.kvh * P.group + g;
             for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
-              const uint32_t st = n % NST;
-              if (!wait_bounded(qd_empty(st), ((n / NST) & 1) ^ 1u, abort_flag, P.wait,
-                                kErrWaitEmpty)) {
+              if (!wait_bounded(q_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
                 ok = false;
                 break;
               }
-              if (n != P.debug_drop) {
-                mbar_arrive_expect_tx(qd_full(st), 2 * TILE_BYTES);
-                load_tile(sQ(st), &mapQ, qd_full(st), head, i * BT, x.shard);
-                load_tile(sdO(st), &mapdO, qd_full(st), head, i * BT, x.shard);
+              mbar_arrive_expect_tx(q_full(n), TILE_BYTES);
+              load_tile(sQ(n), &mapQ, q_full(n), head, i * BT, x.shard);
+              if (!wait_bounded(do_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+                ok = false;
+                ++nq;
+                break;
               }
+              if (n != P.debug_drop) {
+                mbar_arrive_expect_tx(do_full(n), TILE_BYTES);
+                load_tile(sdO(n), &mapdO, do_full(n), head, i * BT, x.shard);
+              }
+              ++nq;
             }
           }
         }
         // Teardown: let the last loads land before shared memory is released.
         if (nu > 0) wait_teardown(kv_full, (nu - 1) & 1, P.wait);
-        for (int64_t q = n > NST ? n - NST : 0; q < n; ++q)
-          if (q != P.debug_drop)
-            wait_teardown(qd_full(static_cast<uint32_t>(q % NST)),
-                          static_cast<uint32_t>((q / NST) & 1), P.wait);
+        for (uint32_t q = nq > NA ? nq - NA : 0; q < nq; ++q) wait_teardown(q_full(q), (q / NA) & 1, P.wait);
+        for (uint32_t q = n > NB ? n - NB : 0; q < n; ++q)
+          if (q != P.debug_drop) wait_teardown(do_full(q), (q / NB) & 1, P.wait);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -391,50 +411,56 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // -------------------------------------------------------- MMA issuer
         uint32_t n = 0, nu = 0;
         bool ok = true;
-        auto wait_qd = [&](uint32_t m) {
-          return wait_bounded(qd_full(m % NST), (m / NST) & 1, abort_flag, P.wait, kErrWaitFull);
+        auto wait_q = [&](uint32_t m) {
+          return wait_bounded(q_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull);
+        };
+        auto wait_do = [&](uint32_t m) {
+          return wait_bounded(do_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull);
         };
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
           const KeyUnit x = key_unit(P, u);
           const int32_t steps = P.group * (x.ib - x.ia);
           if (x.ia >= x.ib) continue;
-          if (!wait_bounded(kv_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_qd(n)) break;
+          if (!wait_bounded(kv_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_q(n)) break;
           tc_fence_after();
-          mma_tiles(tS, sK, sQ(n % NST));
+          mma_tiles(tS, sK, sQ(n));
           tc_commit(s_full);
-          mma_tiles(tdP, sV, sdO(n % NST));
+          if (!wait_do(n)) break;
+          tc_fence_after();
+          mma_tiles(tdP, sV, sdO(n));
           tc_commit(dp_full);
           if (steps == 1) tc_commit(kv_empty);
           for (int32_t s = 0; s < steps; ++s, ++n) {
-            const uint32_t st = n % NST, nx = (n + 1) % NST;
             const bool more = s + 1 < steps;
-            if (!wait_bounded(p_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
+            if (more) {
+              // the next scores as soon as the warps hold this step's
+              if (!wait_bounded(s_free, n & 1, abort_flag, P.wait, kErrWaitAttn) || !wait_q(n + 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              mma_tiles(tS, sK, sQ(n + 1));
+              tc_commit(s_full);
+            }
+            if (!wait_bounded(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
                 (s == 0 && nu > 0 &&
                  !wait_bounded(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            mma_rows(tdV, tS, sdO(st), s > 0);
+            mma_rows(tdV, tdP, sdO(n), s > 0);
+            tc_commit(do_empty(n));
+            mma_rows(tdK, tdP + 16, sQ(n), s > 0);
+            tc_commit(q_empty(n));
             if (more) {
-              if (!wait_qd(n + 1)) {
+              if (!wait_do(n + 1)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              mma_tiles(tS, sK, sQ(nx));
-              tc_commit(s_full);
-            }
-            if (!wait_bounded(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            mma_rows(tdK, tdP, sQ(st), s > 0);
-            tc_commit(qd_empty(st));
-            if (more) {
-              mma_tiles(tdP, sV, sdO(nx));
+              mma_tiles(tdP, sV, sdO(n + 1));
               tc_commit(dp_full);
               if (s + 2 == steps) tc_commit(kv_empty);   // K and V are read by S^T and dP^T alone
             }
@@ -459,48 +485,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int64_t row0 =
               (static_cast<int64_t>(x.shard) * P.hq + x.kvh * P.group + g) * P.T;
           for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
-            const uint32_t st = n % NST;
             const bool cut = !tile_span(P.mask, i, P.tiles, P.T, P.causal).whole(x.kb);
             float lse[2], dl[2];
-            int2 span[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int32_t q = i * BT + h * 64 + me;
               const bool in = q < P.T;
               lse[h] = in ? -kLog2e * P.LSE[row0 + q] : -INFINITY;   // P = 0 behind the last row
               dl[h] = in ? -P.delta[row0 + q] : 0.0f;
-              span[h] = in ? row_span(P.mask, q, P.T, P.causal) : make_int2(0, -1);
             }
-            ok = wait_bounded(qd_empty(st), ((n / NST) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty);
+            ok = wait_bounded(do_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t o = (h * 64 + me) * 4;
-              sts(vec(st, 0) + o, lse[h]);
-              sts(vec(st, 1) + o, dl[h]);
-              sts(vec(st, 2) + o, __int_as_float(span[h].x));
-              sts(vec(st, 3) + o, __int_as_float(span[h].y));
+              sts(vec(n, 0) + (h * 64 + me) * 4, lse[h]);
+              sts(vec(n, 1) + (h * 64 + me) * 4, dl[h]);
             }
-            if (me == 0) cut_flag[st] = cut;
+            if (me == 0) cut_flag[n % NB] = cut;
+            ok = wait_bounded(q_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull) &&
+                 (!cut || wait_bounded(do_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitFull));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             if (cut) {
-              ok = wait_bounded(qd_full(st), (n / NST) & 1, abort_flag, P.wait, kErrWaitFull);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int row = h * 64 + me;
-                const bool b0 = row_not_finite(sQ(st), row), b1 = row_not_finite(sdO(st), row);
-                if (b0) zero_row(sQ(st), row);
-                if (b1) zero_row(sdO(st), row);
+                const bool b0 = row_not_finite(sQ(n), row), b1 = row_not_finite(sdO(n), row);
+                if (b0) zero_row(sQ(n), row);
+                if (b1) zero_row(sdO(n), row);
                 const uint32_t w = __ballot_sync(0xffffffffu, b0 || b1);
-                if (lane == 0) bad[st * 4 + h * 2 + (warp - 2)] = w;
+                if (lane == 0) bad[(n % NB) * 4 + h * 2 + (warp - 2)] = w;
               }
               fence_proxy_async_smem();
             }
-            mbar_arrive(vec_full(st));
+            mbar_arrive(vec_full(n));
             __syncwarp();
-            if (lane == 0) mbar_arrive(qd_empty(st));
+            if (lane == 0) {
+              mbar_arrive(q_empty(n));
+              mbar_arrive(do_empty(n));
+            }
           }
         }
       }
@@ -518,49 +542,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const KeyUnit x = key_unit(P, u);
       if (x.ia >= x.ib) continue;
       const int32_t key = x.kb * BT + quad * 32 + lane;
+      const int2 by = key_span(P.mask, key, P.T, P.causal);   // queries that see the key
       for (int32_t g = 0; ok && g < P.group; ++g) {
         float slope2 = 0.0f;
         if (BIAS) slope2 = kLog2e * P.slopes[x.shard * P.hq + x.kvh * P.group + g];
         for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
-          const uint32_t st = n % NST;
-          ok = wait_bounded(vec_full(st), (n / NST) & 1, abort_flag, P.wait, kErrWaitAttn) &&
+          ok = wait_bounded(vec_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitAttn) &&
                wait_bounded(s_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const bool cut = cut_flag[st] != 0;
-          const uint32_t vl = vec(st, 0) + part * 128, vd = vec(st, 1) + part * 128;
-          const uint32_t va = vec(st, 2) + part * 128, vb = vec(st, 3) + part * 128;
-          const float dist0 = static_cast<float>(i * BT + part * 32 - key);
-          const int side = i * BT >= x.kb * BT + BT - 1 ? 1 : i * BT + BT - 1 <= x.kb * BT ? -1 : 0;
           float w[32];
+          uint32_t v[32], pk[16];
+          tmem_ld_32x32b_x32(tS + off, v);
+          const bool cut = cut_flag[n % NB] != 0;
+          const uint32_t vl = vec(n, 0) + part * 128, vd = vec(n, 1) + part * 128;
+          const int32_t q0 = i * BT + part * 32;
+          const float dist0 = static_cast<float>(q0 - key);
+          const int side = i * BT >= x.kb * BT + BT - 1 ? 1 : i * BT + BT - 1 <= x.kb * BT ? -1 : 0;
           uint32_t seen = 0xffffffffu;   // columns that see this key
           if (cut) {
-            seen = 0;
-            for (int e = 0; e < 32; ++e) {
-              const int32_t a = __float_as_int(lds(va + e * 4)), b = __float_as_int(lds(vb + e * 4));
-              seen |= static_cast<uint32_t>(key >= a && key < b) << e;
-            }
-            if (seen & bad[st * 4 + part]) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
+            const int32_t lo = min(max(by.x - q0, 0), 32), hi = min(max(by.y - q0, 0), 32);
+            seen = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+            if (seen & bad[(n % NB) * 4 + part]) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
           }
-          uint32_t v[32], pk[16];
           auto sees = [&](int e) { return ((seen >> e) & 1u) != 0; };
-          tmem_ld_32x32b_x32(tS + off, v);
           tmem_ld_wait();
+          tc_fence_before();
+          mbar_arrive(s_free);
           prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut,
                                 [&](int e) { return lds2(vl + e * 4); }, sees);
-          tmem_st_32x32b_x16(tS + off, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(p_full);
           ok = wait_bounded(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           tmem_ld_32x32b_x32(tdP + off, v);
           tmem_ld_wait();
-          grad_chunk(v, w, pk, cut, [&](int e) { return lds2(vd + e * 4); }, sees);
+          // P^T and dS^T over this quarter's own dP^T
           tmem_st_32x32b_x16(tdP + off, pk);
+          grad_chunk(v, w, pk, cut, [&](int e) { return lds2(vd + e * 4); }, sees);
+          tmem_st_32x32b_x16(tdP + off + 16, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(ds_full);
@@ -572,7 +593,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       // keys of no document stay as they were
-      const bool store = key < P.T && row_span(P.mask, key, P.T, P.causal).y >= 0;
+      const bool store = key < P.T && by.y >= 0;
       const int64_t row =
           ((static_cast<int64_t>(x.shard) * P.T + key) * P.hkv + x.kvh) * DH + part * 32;
       const uint32_t hits = *const_cast<volatile uint32_t*>(&hit[(nu % 3) * 4 + quad]);
@@ -616,36 +637,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const __grid_constant__ CUtensorMap mapV,
                         const __grid_constant__ CUtensorMap mapdO,
                         const __grid_constant__ BwdParams P) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);
+  if ((base & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(P.wait.err, kErrSmem);
+    return;
+  }
   const uint32_t sQ = base, sdO = base + TILE_BYTES;
-  auto sK = [&](uint32_t st) { return base + 2 * TILE_BYTES + st * 2 * TILE_BYTES; };
-  auto sV = [&](uint32_t st) { return sK(st) + TILE_BYTES; };
-  uint8_t* const ctrl = smem_raw + (base - raw) + 2 * TILE_BYTES + NST * 2 * TILE_BYTES;
+  auto sK = [&](uint32_t n) { return base + (2 + n % NA) * TILE_BYTES; };
+  auto sV = [&](uint32_t n) { return base + (2 + NA + n % NB) * TILE_BYTES; };
+  uint8_t* const ctrl = smem_raw + TILES_BYTES;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl);
   const uint32_t qd_full = smem_u32(&bars[0]), qd_empty = smem_u32(&bars[1]);
-  auto kv_full = [&](uint32_t s) { return smem_u32(&bars[2 + s]); };
-  auto kv_empty = [&](uint32_t s) { return smem_u32(&bars[4 + s]); };
-  auto s_full = [&](uint32_t b) { return smem_u32(&bars[6 + b]); };
-  const uint32_t dp_full = smem_u32(&bars[8]), dp_free = smem_u32(&bars[9]);
-  const uint32_t ds_full = smem_u32(&bars[10]);
-  const uint32_t acc_full = smem_u32(&bars[11]), acc_empty = smem_u32(&bars[12]);
-  auto k_seen = [&](uint32_t i) { return smem_u32(&bars[13 + i]); };
-  const uint32_t drain = smem_u32(&bars[15]);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 16);
+  auto k_full = [&](uint32_t n) { return smem_u32(&bars[2 + n % NA]); };
+  auto k_empty = [&](uint32_t n) { return smem_u32(&bars[5 + n % NA]); };
+  auto v_full = [&](uint32_t n) { return smem_u32(&bars[8 + n % NB]); };
+  auto v_empty = [&](uint32_t n) { return smem_u32(&bars[10 + n % NB]); };
+  auto s_full = [&](uint32_t b) { return smem_u32(&bars[12 + b]); };
+  const uint32_t dp_full = smem_u32(&bars[14]), dp_free = smem_u32(&bars[15]);
+  const uint32_t ds_full = smem_u32(&bars[16]);
+  const uint32_t acc_full = smem_u32(&bars[17]), acc_empty = smem_u32(&bars[18]);
+  // one a ring slot: warps 2 and 3 may be that many blocks ahead
+  auto k_seen = [&](uint32_t i) { return smem_u32(&bars[19 + i % NA]); };
+  const uint32_t drain = smem_u32(&bars[19 + NA]);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (20 + NA));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     mbar_init(qd_full, 1);
     mbar_init(qd_empty, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(kv_full(s), 1);
-      mbar_init(kv_empty(s), 3);   // the MMA thread's commit, warps 2 and 3
-      mbar_init(s_full(s), 1);
+    for (int s = 0; s < NA; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 3);   // the MMA thread's commit, warps 2 and 3
       mbar_init(k_seen(s), 64);
     }
+    for (int s = 0; s < NB; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(s_full(s), 1);
     mbar_init(dp_full, 1);
     mbar_init(dp_free, ARITH);
     mbar_init(ds_full, ARITH);
@@ -678,8 +709,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 0) {
       if (lane == 0) {
         // ---------------------------------------------------------- producer
-        uint32_t nu = 0;
-        int64_t n = 0;
+        uint32_t nu = 0, n = 0, nk = 0;   // nk: loads of K
         bool ok = true;
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
@@ -691,23 +721,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           load_tile(sdO, &mapdO, qd_full, x.head, x.qb * BT, x.shard);
           ++nu;
           for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
-            const uint32_t st = n % NST;
-            if (!wait_bounded(kv_empty(st), ((n / NST) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+            if (!wait_bounded(k_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(k_full(n), TILE_BYTES);
+            load_tile(sK(n), &mapK, k_full(n), x.kvh, j * BT, x.shard);
+            ++nk;
+            if (!wait_bounded(v_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
               ok = false;
               break;
             }
             if (n != P.debug_drop) {
-              mbar_arrive_expect_tx(kv_full(st), 2 * TILE_BYTES);
-              load_tile(sK(st), &mapK, kv_full(st), x.kvh, j * BT, x.shard);
-              load_tile(sV(st), &mapV, kv_full(st), x.kvh, j * BT, x.shard);
+              mbar_arrive_expect_tx(v_full(n), TILE_BYTES);
+              load_tile(sV(n), &mapV, v_full(n), x.kvh, j * BT, x.shard);
             }
           }
         }
         if (nu > 0) wait_teardown(qd_full, (nu - 1) & 1, P.wait);
-        for (int64_t q = n > NST ? n - NST : 0; q < n; ++q)
-          if (q != P.debug_drop)
-            wait_teardown(kv_full(static_cast<uint32_t>(q % NST)),
-                          static_cast<uint32_t>((q / NST) & 1), P.wait);
+        for (uint32_t q = nk > NA ? nk - NA : 0; q < nk; ++q) wait_teardown(k_full(q), (q / NA) & 1, P.wait);
+        for (uint32_t q = n > NB ? n - NB : 0; q < n; ++q)
+          if (q != P.debug_drop) wait_teardown(v_full(q), (q / NB) & 1, P.wait);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -715,40 +749,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // -------------------------------------------------------- MMA issuer
         uint32_t n = 0, nu = 0;
         bool ok = true;
-        auto wait_kv = [&](uint32_t m) {
-          return wait_bounded(kv_full(m % NST), (m / NST) & 1, abort_flag, P.wait, kErrWaitFull);
-        };
         auto issue_s = [&](uint32_t m) {
-          mma_tiles(tm + (m & 1) * 128, sQ, sK(m % NST));
+          if (!wait_bounded(k_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
+          tc_fence_after();
+          mma_tiles(tm + (m & 1) * 128, sQ, sK(m));
           tc_commit(s_full(m & 1));
+          return true;
+        };
+        auto issue_dp = [&](uint32_t m) {
+          if (!wait_bounded(v_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
+          tc_fence_after();
+          mma_tiles(tdP, sdO, sV(m));
+          tc_commit(v_empty(m));
+          tc_commit(dp_full);
+          return true;
         };
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
           const QueryUnit x = query_unit(P, u);
           const int32_t steps = x.t.je - x.t.jb;
           if (steps <= 0) continue;
-          if (!wait_bounded(qd_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_kv(n)) break;
-          tc_fence_after();
-          issue_s(n);
-          mma_tiles(tdP, sdO, sV(n % NST));
-          tc_commit(dp_full);
-          if (steps == 1) {
+          if (!wait_bounded(qd_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !issue_s(n) ||
+              !issue_dp(n))
+            break;
+          if (steps == 1)
             tc_commit(qd_empty);
-          } else {
-            if (!wait_kv(n + 1)) break;
-            tc_fence_after();
-            issue_s(n + 1);
-          }
+          else if (!issue_s(n + 1))
+            break;
           for (int32_t s = 0; s < steps; ++s, ++n) {
             if (s + 1 < steps) {
               // the warps have read dP of this step
-              if (!wait_bounded(dp_free, n & 1, abort_flag, P.wait, kErrWaitAttn)) {
-                ok = false;
-                break;
+              ok = wait_bounded(dp_free, n & 1, abort_flag, P.wait, kErrWaitAttn);
+              if (ok) {
+                tc_fence_after();
+                ok = issue_dp(n + 1);
               }
-              tc_fence_after();
-              mma_tiles(tdP, sdO, sV((n + 1) % NST));
-              tc_commit(dp_full);
+              if (!ok) break;
               if (s + 2 == steps) tc_commit(qd_empty);
             }
             if (!wait_bounded(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
@@ -758,15 +794,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               break;
             }
             tc_fence_after();
-            mma_rows(tdQ, tm + (n & 1) * 128, sK(n % NST), s > 0);
-            tc_commit(kv_empty(n % NST));
-            if (s + 2 < steps) {
-              if (!wait_kv(n + 2)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              issue_s(n + 2);
+            mma_rows(tdQ, tm + (n & 1) * 128, sK(n), s > 0);
+            tc_commit(k_empty(n));
+            if (s + 2 < steps && !issue_s(n + 2)) {
+              ok = false;
+              break;
             }
           }
           if (!ok) break;
@@ -785,22 +817,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
         const QueryUnit x = query_unit(P, u);
         for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
-          const uint32_t st = n % NST;
-          ok = wait_bounded(kv_full(st), (n / NST) & 1, abort_flag, P.wait, kErrWaitFull);
+          ok = wait_bounded(k_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (!x.t.whole(j)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int row = h * 64 + (warp - 2) * 32 + lane;
-              if (row_not_finite(sK(st), row)) zero_row(sK(st), row);
+              if (row_not_finite(sK(n), row)) zero_row(sK(n), row);
             }
             fence_proxy_async_smem();
-            mbar_arrive(k_seen(looked & 1));
+            mbar_arrive(k_seen(looked));
             ++looked;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(kv_empty(st));
+          if (lane == 0) mbar_arrive(k_empty(n));
         }
       }
     }
@@ -830,7 +861,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool cut = !x.t.whole(j);
         ok = wait_bounded(s_full(b), (n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn);
         if (cut) {
-          ok = ok && wait_bounded(k_seen(looked & 1), (looked >> 1) & 1, abort_flag, P.wait, kErrWaitAttn);
+          ok = ok && wait_bounded(k_seen(looked), (looked / NA) & 1, abort_flag, P.wait, kErrWaitAttn);
           ++looked;
         }
         ok = __all_sync(0xffffffffu, ok);

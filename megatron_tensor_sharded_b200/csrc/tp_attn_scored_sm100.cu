@@ -606,6 +606,7 @@ __global__ void __launch_bounds__(kAttnTile)
   pdl_launch_dependents();
   const int32_t t = blockIdx.x * kAttnTile + threadIdx.x;
   int32_t lo = 0, hi = -1;
+  int2 by = make_int2(0, -1);
   if (t < T) {
     int32_t a = 0, b = n_docs + 1;   // the last offset <= t is below b
     while (b - a > 1) {
@@ -620,13 +621,16 @@ __global__ void __launch_bounds__(kAttnTile)
       if (ds <= t && t < de) {
         lo = ds;
         hi = de;
+        by = make_int2(ds, de);
         if (causal) {
           const int32_t free = prefix != nullptr ? min(max(prefix[a], 0), de - ds) : 0;
           hi = max(t + 1, ds + free);
+          if (t >= ds + free) by.x = t;
         }
       }
     }
     plan.rows[t] = make_int2(lo, hi);
+    plan.keys[t] = by;
   }
   const bool in = hi >= 0;
   int32_t v[4] = {in ? lo : INT_MAX, in ? hi : 0, t < T ? lo : 0, t < T ? hi : INT_MAX};

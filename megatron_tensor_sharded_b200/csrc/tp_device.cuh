@@ -17,6 +17,7 @@ constexpr unsigned kErrWaitAccEmpty = 1u << 3;  // mma: accumulator never draine
 constexpr unsigned kErrWaitDrain = 1u << 4;     // teardown: in-flight work never finished
 constexpr unsigned kErrWaitRegion = 1u << 7;    // fold: a region's partial tiles never completed
 
+constexpr unsigned kErrSmem = 1u << 9;          // dynamic shared memory does not start at 1024 bytes
 constexpr unsigned kErrLength = 1u << 8;        // decode: a sequence longer than its cache
 
 struct WaitCtl {

@@ -47,6 +47,12 @@ __device__ __forceinline__ int2 row_span(const MaskPlan& m, int32_t q, int32_t T
   return make_int2(0, causal ? min(q + 1, T) : T);
 }
 
+// Queries [x, y) that see key k; y < 0: the key lies in no document.
+__device__ __forceinline__ int2 key_span(const MaskPlan& m, int32_t k, int32_t T, int32_t causal) {
+  if (m.rows != nullptr) return k < T ? m.keys[k] : make_int2(0, -1);
+  return make_int2(causal ? k : 0, T);
+}
+
 // 32 raw products -> capped scores in log2 units.  True where the warp took
 // the MUFU form (some row's |scale s| > cap/2, or a NaN).
 __device__ __forceinline__ bool cap_chunk(uint32_t* v, const ScoreConsts& S) {

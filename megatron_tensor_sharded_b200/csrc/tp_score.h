@@ -16,9 +16,11 @@ constexpr int kAttnTile = 128;   // query rows and key rows of a tile
 // The mask's plan (tp_attention_mask): per query row the keys it sees, [x, y)
 // (y < 0: the row lies in no document); per tile of 128 query rows {least x,
 // greatest y, greatest x, least y}, the first two over rows in a document; per
-// tile of 128 keys the query tiles [x, y) that may see one of them.
+// key the queries [x, y) that see it, and per tile of 128 keys the query tiles
+// [x, y) that may see one of them.
 struct MaskPlan {
   int2* rows;
+  int2* keys;
   int4* q_tiles;
   int2* k_tiles;
 };
@@ -28,12 +30,13 @@ inline MaskPlan mask_plan(const void* buf, int64_t T) {
   const size_t tiles = static_cast<size_t>(ceil_div(T, kAttnTile));
   uint8_t* b = static_cast<uint8_t*>(const_cast<void*>(buf));
   const size_t r = mask_align(static_cast<size_t>(T) * sizeof(int2));
-  return MaskPlan{reinterpret_cast<int2*>(b), reinterpret_cast<int4*>(b + r),
-                  reinterpret_cast<int2*>(b + r + mask_align(tiles * sizeof(int4)))};
+  return MaskPlan{reinterpret_cast<int2*>(b), reinterpret_cast<int2*>(b + r),
+                  reinterpret_cast<int4*>(b + 2 * r),
+                  reinterpret_cast<int2*>(b + 2 * r + mask_align(tiles * sizeof(int4)))};
 }
 inline size_t mask_bytes(int64_t T) {
   const size_t tiles = static_cast<size_t>(ceil_div(T, kAttnTile));
-  return mask_align(static_cast<size_t>(T) * sizeof(int2)) + mask_align(tiles * sizeof(int4)) +
+  return 2 * mask_align(static_cast<size_t>(T) * sizeof(int2)) + mask_align(tiles * sizeof(int4)) +
          mask_align(tiles * sizeof(int2));
 }
 

@@ -62,7 +62,7 @@ def _call(case, dev, score, O, LSE):
     return g
 
 
-def _check(case, host, slopes, seen, inside, O, LSE, grads, rows=None):
+def _check(case, host, slopes, seen, inside, O, LSE, grads, rows=None, kv_heads=None):
     p, T, hq, hk = case["p"], case["T"], case["h"] // case["p"], case["hkv"] // case["p"]
     Q, K, V, dO = host
     O, LSE = O.double().cpu().numpy(), LSE.double().cpu().numpy()
@@ -72,6 +72,8 @@ def _check(case, host, slopes, seen, inside, O, LSE, grads, rows=None):
     u = S.U
     for i in range(p):
         for n in range(hk):
+            if kv_heads is not None and (i, n) not in kv_heads:
+                continue
             k, v = S.head(K, i, n), S.head(V, i, n)
             sums = [np.zeros((T, 128)) for _ in range(4)]     # dk, dv and their bounds
             for j in range(n * group, n * group + group):
@@ -131,6 +133,18 @@ def test_forward_then_backward_gives_the_true_gradient(case):
     for a, b in zip(got, want):
         a, b = a[:, inside], b[:, inside]
         assert np.linalg.norm(a - b) <= 4 * S.U * np.linalg.norm(b)
+
+
+@pytest.mark.parametrize("case", [
+    dict(p=2, T=700, h=48, hkv=48, off=[0, 1, 128, 129, 384, 650], slopes=1.0),
+    dict(p=1, T=600, h=64, hkv=64, off=list(range(0, 601, 25)), cap=30.0),
+    dict(p=2, T=500, h=64, hkv=64, cap=50.0)], ids=["docs", "short", "causal"])
+def test_several_units_a_block_of_threads(case):
+    """More (head, tile) units than the GPU has SMs, masks in most blocks."""
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case, seed=2)
+    grads = _call(case, dev, score, O, LSE)
+    last = (case["p"] - 1, case["hkv"] // case["p"] - 1)
+    _check(case, host, slopes, seen, inside, O, LSE, grads, kv_heads={(0, 0), (0, 7), last})
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
