@@ -73,6 +73,14 @@ __device__ __forceinline__ int64_t tiles_of(int32_t keys) {
   return keys <= 0 ? 0 : (keys + TILE - 1) / TILE;
 }
 
+// First tile of CTA c's share of `total` tiles (both below 2^31 in sum with
+// the CTAs' number in almost every call: 32-bit division then).
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t c, int32_t ctas) {
+  const uint64_t x = static_cast<uint64_t>(total) * static_cast<uint64_t>(c);
+  if (x >> 32) return static_cast<int64_t>(x / static_cast<uint32_t>(ctas));
+  return static_cast<uint32_t>(x) / static_cast<uint32_t>(ctas);
+}
+
 // Sum of v over the CTA's threads; every thread gets it (and, in *before, the
 // sum over the threads of a lower number).
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* before, int64_t* scratch) {
@@ -156,27 +164,33 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
   pdl_wait();
   pdl_launch_dependents();
 
-  // The line's length, then the place of this CTA's first tile on it.
-  int64_t total = 0, before;
+  // The line's length, then the place of this CTA's first tile on it (one
+  // pass over the lengths where there are no more than threads).
+  int64_t total = 0, before = 0;
+  int32_t keys = 0;
   bool bad = false;
   for (int32_t b0 = 0; b0 < P.B; b0 += WARPS * 32) {
     const int32_t b = b0 + threadIdx.x;
-    const int32_t keys = b < P.B ? keys_of(P, b) : 0;
+    keys = b < P.B ? keys_of(P, b) : 0;
     bad |= keys == -2;
     total += block_sum(tiles_of(keys) * P.heads, &before, scratch);
   }
   if (bad && blockIdx.x == 0) atomicOr(P.err, kErrLength);
-  const int64_t w0 = total * blockIdx.x / P.ctas, w1 = total * (blockIdx.x + 1) / P.ctas;
+  const int64_t w0 = share_of(total, blockIdx.x, P.ctas), w1 = share_of(total, blockIdx.x + 1, P.ctas);
   if (w0 >= w1) return;
   int64_t done = 0;
   for (int32_t b0 = 0; b0 < P.B && done <= w0; b0 += WARPS * 32) {
     const int32_t b = b0 + threadIdx.x;
-    const int32_t keys = b < P.B ? keys_of(P, b) : 0;
-    const int64_t tiles = tiles_of(keys), mine = tiles * P.heads;
-    const int64_t sum = block_sum(mine, &before, scratch);
-    const int64_t at = w0 - (done + before);
-    if (mine > 0 && at >= 0 && at < mine)
-      start = Place{b, static_cast<int32_t>(at / tiles), keys, at % tiles, tiles};
+    int64_t sum = total;
+    if (P.B > WARPS * 32) {
+      keys = b < P.B ? keys_of(P, b) : 0;
+      sum = block_sum(tiles_of(keys) * P.heads, &before, scratch);
+    }
+    const int64_t tiles = tiles_of(keys), at = w0 - (done + before);
+    if (tiles > 0 && at >= 0 && at < tiles * P.heads) {
+      const int32_t h = static_cast<int32_t>(static_cast<uint32_t>(at) / static_cast<uint32_t>(tiles));
+      start = Place{b, h, keys, at - h * tiles, tiles};
+    }
     done += sum;
   }
   __syncthreads();
@@ -435,19 +449,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
   const int32_t in_group = mt * MROWS + blockIdx.y;
   if (in_group >= P.group) return;
-  pdl_wait();
-  pdl_launch_dependents();
+  // The lengths were complete before the decode kernel, which this one waits
+  // for, let it start: where the parts lie is worked out beside it.
   const int32_t keys = keys_of(P, b);
-  if (keys < 0) return;
   const int32_t head = kvh * P.group + in_group, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   __nv_bfloat16* const out = P.O + ((static_cast<int64_t>(shard) * P.B + b) * P.hq + head) * DH;
   float* const lse =
       P.LSE != nullptr ? P.LSE + (static_cast<int64_t>(shard) * P.hq + head) * P.B + b : nullptr;
-  if (keys == 0) {
-    if (warp == 0) *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(0, 0);
-    if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
-    return;
-  }
   int64_t total = 0, ahead = 0, before;
   for (int32_t b0 = 0; b0 < P.B; b0 += JOIN_THREADS) {
     const int32_t i = b0 + threadIdx.x;
@@ -457,16 +465,29 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   }
   const int64_t tiles = tiles_of(keys), a = ahead + h * tiles, z = a + tiles - 1;
   // the CTA of tile w: the last c with total * c / ctas <= w
-  auto cta_of = [&](int64_t w) { return ((w + 1) * P.ctas - 1) / total; };
-  const int64_t c0 = cta_of(a), c1 = cta_of(z);
+  auto cta_of = [&](int64_t w) {
+    const uint64_t x = static_cast<uint64_t>(w + 1) * P.ctas - 1;
+    if ((x | static_cast<uint64_t>(total)) >> 32) return static_cast<int64_t>(x / total);
+    return static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(total));
+  };
+  const int64_t c0 = keys > 0 ? cta_of(a) : 0, c1 = keys > 0 ? cta_of(z) : 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (keys < 0) return;
+  if (keys == 0) {
+    if (warp == 0) *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(0, 0);
+    if (threadIdx.x == 0 && lse != nullptr) *lse = -INFINITY;
+    return;
+  }
   if (c0 == c1) return;   // written whole
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int64_t c = c0 + warp; c <= c1; c += JOIN_THREADS / 32) {
-    if (total * c / P.ctas == total * (c + 1) / P.ctas) continue;   // fewer tiles than CTAs
+    const int64_t first = share_of(total, c, P.ctas);
+    if (first == share_of(total, c + 1, P.ctas)) continue;   // fewer tiles than CTAs
     // a CTA's first item is its slot 0; the item begins inside c0 unless it
     // begins with it
-    const bool second = c == c0 && total * c / P.ctas != a;
+    const bool second = c == c0 && first != a;
     const float* part = P.part + (c * 2 + (second ? 1 : 0)) * PART_FLOATS;
     const float pm = part[MROWS * DH + blockIdx.y], pl = part[MROWS * DH + MROWS + blockIdx.y];
     const float4 x = *reinterpret_cast<const float4*>(part + blockIdx.y * DH + lane * 4);

@@ -224,31 +224,43 @@ __device__ __forceinline__ void sts(uint32_t addr, float v) {
 }
 
 // ------------------------------------------------------------------ delta
-// D[shard][head][t] = sum over the head of dO * O: 16 lanes a row.
+// D[shard][head][t] = sum over the head of dO * O: 16 lanes a row, four rows of
+// each lane loaded together.
+constexpr int DELTA_ROWS = 64;   // rows of a CTA
 __global__ void __launch_bounds__(256)
     score_delta_kernel(const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
                        float* __restrict__ delta, int64_t rows, int32_t T, int32_t hq) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;   // [shard][t][head]
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * DELTA_ROWS + threadIdx.x / 16;   // [shard][t][head]
   const int lane = threadIdx.x % 16;
-  float s = 0.0f;
-  if (row < rows) {
-    const uint4 a = *reinterpret_cast<const uint4*>(O + row * DH + lane * 8);
-    const uint4 b = *reinterpret_cast<const uint4*>(dO + row * DH + lane * 8);
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  uint4 a[4], b[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int64_t row = row0 + n * 16;
+    a[n] = b[n] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      a[n] = *reinterpret_cast<const uint4*>(O + row * DH + lane * 8);
+      b[n] = *reinterpret_cast<const uint4*>(dO + row * DH + lane * 8);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int64_t row = row0 + n * 16;
+    const uint32_t x[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, y[4] = {b[n].x, b[n].y, b[n].z, b[n].w};
+    float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       s += __uint_as_float(x[i] << 16) * __uint_as_float(y[i] << 16);
       s += __uint_as_float(x[i] & 0xffff0000u) * __uint_as_float(y[i] & 0xffff0000u);
     }
-  }
 #pragma unroll
-  for (int o = 8; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (row < rows && lane == 0) {
-    const int64_t st = row / hq;            // shard * T + t
-    const int64_t shard = st / T;
-    delta[(shard * hq + row % hq) * T + (st - shard * T)] = s;
+    for (int o = 8; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (row < rows && lane == 0) {
+      const int64_t st = row / hq;            // shard * T + t
+      const int64_t shard = st / T;
+      delta[(shard * hq + row % hq) * T + (st - shard * T)] = s;
+    }
   }
 }
 
@@ -964,7 +976,8 @@ tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a) {
     return TP_ERR_CUDA;
   const int64_t rows = a.T * a.p * a.hq;
   const cudaError_t e =
-      launch_pdl(score_delta_kernel, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0,
+      launch_pdl(score_delta_kernel, dim3(static_cast<unsigned>((rows + DELTA_ROWS - 1) / DELTA_ROWS)),
+                 dim3(256), 0,
                  c.stream, static_cast<const __nv_bfloat16*>(a.O),
                  static_cast<const __nv_bfloat16*>(a.dO), a.delta, rows, static_cast<int32_t>(a.T),
                  static_cast<int32_t>(a.hq));

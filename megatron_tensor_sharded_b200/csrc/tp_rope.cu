@@ -56,24 +56,42 @@ struct RopeParams {
   uint64_t turn[kMaxPairs];        // fraction of a turn per position, 2^-64 units
 };
 
-template <typename E>
-__device__ __forceinline__ void load8(const E* p, float (&v)[8]);
-template <>
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+// Eight elements as they came from memory: loads are issued together and
+// converted where they are used.
+template <typename E>
+struct Raw8;
 template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
   }
-}
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
 template <typename E>
 __device__ __forceinline__ void store8(E* p, const float (&v)[8]);
 template <>
@@ -137,8 +155,8 @@ __device__ __forceinline__ Chunk chunk_of(const RopeParams& P, int32_t u) {
 __device__ __forceinline__ void rotate(const float* cs, const float* sn, bool interleaved,
                                        float (&a)[8], float (&b)[8]) {
   float c[8], s[8];
-  load8<float>(cs, c);
-  load8<float>(sn, s);
+  load8(cs, c);
+  load8(sn, s);
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -180,69 +198,73 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
   const int32_t w0 = blockIdx.y * P.row_split, nw = min(P.row_split, rows - w0);
   const int32_t total = ntok * nw;
   const Chunk c = chunk_of(P, threadIdx.x % L);
-  struct Row {
-    float a[8], b[8];
-    int64_t off;
-    int32_t tl;
-    bool k, live;
-  };
-  auto fetch = [&](int32_t i, Row& x) {
-    x.live = i < total && c.live;
-    if (i >= total) i = 0;
-    x.tl = i / nw;
-    int32_t w = w0 + i - x.tl * nw;
-    x.k = w >= qrows;
-    if (x.k) w -= qrows;
-    x.off = row_offset(P, t0 + x.tl, w, x.k ? P.hk : P.hq);
+  // BATCH rows of a thread are loaded together (enough bytes in flight to
+  // cover the latency of HBM), the first ones before the angles are computed
+  constexpr int BATCH = sizeof(E) == 2 ? 4 : 2;
+  for (int32_t base = 0; base < total; base += BATCH * ROWS) {
+    Raw8<E> ra[BATCH], rb[BATCH];
+    int64_t off[BATCH];
+    int32_t tl[BATCH];
+    bool isk[BATCH];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x.a[e] = x.b[e] = 0.0f;
-    if (x.live) {
-      const E* src = static_cast<const E*>(x.k ? P.K : P.Q) + x.off;
-      load8<E>(src + c.lo, x.a);
-      load8<E>(src + c.hi, x.b);
-    }
-  };
-  Row cur;
-  fetch(threadIdx.x / L, cur);
-  fill_angles(P, t0, ntok, cs, sn);
-  __syncthreads();
-  for (int32_t i = threadIdx.x / L; i - static_cast<int32_t>(threadIdx.x / L) < total; i += ROWS) {
-    Row nxt;
-    const bool more = i - static_cast<int32_t>(threadIdx.x / L) + ROWS < total;
-    if (more) fetch(i + ROWS, nxt);
-    if (NORM) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += cur.a[e] * cur.a[e] + cur.b[e] * cur.b[e];
-      ss = sum_lanes<L>(ss);
-      const float rstd = rsqrtf(ss / static_cast<float>(P.dh) + P.eps);
-      const float* w = cur.k ? P.wk : P.wq;
-      if (w != nullptr && c.live) {
-        float wl[8], wh[8];
-        load8<float>(w + c.lo, wl);
-        load8<float>(w + c.hi, wh);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          cur.a[e] = cur.a[e] * rstd * wl[e];
-          cur.b[e] = cur.b[e] * rstd * wh[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          cur.a[e] *= rstd;
-          cur.b[e] *= rstd;
-        }
+    for (int n = 0; n < BATCH; ++n) {
+      const int32_t i = base + n * ROWS + threadIdx.x / L;
+      const bool in = i < total && c.live;
+      tl[n] = in ? i / nw : 0;
+      int32_t w = in ? w0 + i - tl[n] * nw : 0;
+      isk[n] = w >= qrows;
+      if (isk[n]) w -= qrows;
+      off[n] = in ? row_offset(P, t0 + tl[n], w, isk[n] ? P.hk : P.hq) : -1;
+      ra[n].zero();
+      rb[n].zero();
+      if (in) {
+        const E* src = static_cast<const E*>(isk[n] ? P.K : P.Q) + off[n];
+        ra[n].load(src + c.lo);
+        rb[n].load(src + c.hi);
       }
     }
-    if (c.turn)
-      rotate(cs + cur.tl * kMaxPairs + c.pair0, sn + cur.tl * kMaxPairs + c.pair0, P.interleaved,
-             cur.a, cur.b);
-    if (cur.live) {
-      E* dst = static_cast<E*>(cur.k ? P.Ko : P.Qo) + cur.off;
-      store8<E>(dst + c.lo, cur.a);
-      store8<E>(dst + c.hi, cur.b);
+    if (base == 0) {
+      fill_angles(P, t0, ntok, cs, sn);
+      __syncthreads();
     }
-    if (more) cur = nxt;
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      float va[8], vb[8];
+      ra[n].get(va);
+      rb[n].get(vb);
+      if (NORM) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += va[e] * va[e] + vb[e] * vb[e];
+        ss = sum_lanes<L>(ss);
+        const float rstd = rsqrtf(ss / static_cast<float>(P.dh) + P.eps);
+        const float* w = isk[n] ? P.wk : P.wq;
+        if (w != nullptr && c.live) {
+          float wl[8], wh[8];
+          load8(w + c.lo, wl);
+          load8(w + c.hi, wh);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            va[e] = va[e] * rstd * wl[e];
+            vb[e] = vb[e] * rstd * wh[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            va[e] *= rstd;
+            vb[e] *= rstd;
+          }
+        }
+      }
+      if (c.turn)
+        rotate(cs + tl[n] * kMaxPairs + c.pair0, sn + tl[n] * kMaxPairs + c.pair0, P.interleaved, va,
+               vb);
+      if (off[n] >= 0) {
+        E* dst = static_cast<E*>(isk[n] ? P.Ko : P.Qo) + off[n];
+        store8<E>(dst + c.lo, va);
+        store8<E>(dst + c.hi, vb);
+      }
+    }
   }
 }
 
@@ -345,9 +367,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = 0.0f;
   for (int32_t t0 = blockIdx.x * P.tok; t0 < P.T; t0 += gridDim.x * P.tok) {
     const int32_t ntok = min(P.tok, P.T - t0);
-    __syncthreads();   // the angles of the previous tokens are no longer read
-    fill_angles(P, t0, ntok, cs, sn);
-    __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int32_t h = k ? P.hk : P.hq, nw = P.p * h;
@@ -355,41 +374,61 @@ __global__ void __launch_bounds__(kThreads, 2)
       const E* DY = static_cast<const E*>(k ? P.dYk : P.dYq);
       E* DX = static_cast<E*>(k ? P.Ko : P.Qo);
       const float* wt = k ? P.wk : P.wq;
-      float w[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = 1.0f;
-      if (wt != nullptr && c.live) {
-        float wl[8], wh[8];
-        load8<float>(wt + c.lo, wl);
-        load8<float>(wt + c.hi, wh);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[e] = wl[e];
-          w[8 + e] = wh[e];
+      const int32_t total = ntok * nw;
+      struct Row {
+        Raw8<E> xa, xb, ga, gb;
+        int64_t off;
+        int32_t tl;
+      };
+      auto fetch = [&](int32_t i, Row& r) {
+        const bool in = i < total && c.live;
+        r.tl = in ? i / nw : 0;
+        r.off = in ? row_offset(P, t0 + r.tl, i - r.tl * nw, h) : -1;
+        r.xa.zero();
+        r.xb.zero();
+        r.ga.zero();
+        r.gb.zero();
+        if (in) {
+          r.xa.load(X + r.off + c.lo);
+          r.xb.load(X + r.off + c.hi);
+          r.ga.load(DY + r.off + c.lo);
+          r.gb.load(DY + r.off + c.hi);
         }
+      };
+      Row cur;
+      fetch(threadIdx.x / L, cur);
+      if (k == 0) {   // (the first rows are on their way)
+        __syncthreads();   // the angles of the previous tokens are no longer read
+        fill_angles(P, t0, ntok, cs, sn);
+        __syncthreads();
       }
-      for (int32_t base = 0; base < ntok * nw; base += ROWS) {
-        const int32_t i = base + threadIdx.x / L;
-        const bool live = i < ntok * nw && c.live;
-        float xa[8] = {}, xb[8] = {}, ga[8] = {}, gb[8] = {};
-        int32_t tl = 0;
-        int64_t off = 0;
-        if (live) {
-          tl = i / nw;
-          off = row_offset(P, t0 + tl, i - tl * nw, h);
-          load8<E>(X + off + c.lo, xa);
-          load8<E>(X + off + c.hi, xb);
-          load8<E>(DY + off + c.lo, ga);
-          load8<E>(DY + off + c.hi, gb);
-          if (c.turn)
-            rotate(cs + tl * kMaxPairs + c.pair0, sn + tl * kMaxPairs + c.pair0, P.interleaved, ga,
-                   gb);
+      for (int32_t base = 0; base < total; base += ROWS) {
+        Row nxt;
+        // (fp32 rows take twice the registers: loaded where they are used)
+        const bool more = base + ROWS < total;
+        if (sizeof(E) == 2 && more) fetch(base + ROWS + threadIdx.x / L, nxt);
+        const bool live = cur.off >= 0;
+        const int64_t off = cur.off;
+        float xa[8], xb[8], ga[8], gb[8];
+        cur.xa.get(xa);
+        cur.xb.get(xb);
+        cur.ga.get(ga);
+        cur.gb.get(gb);
+        if (c.turn)
+          rotate(cs + cur.tl * kMaxPairs + c.pair0, sn + cur.tl * kMaxPairs + c.pair0,
+                 P.interleaved, ga, gb);
+        float wa[8], wb[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
+        if (wt != nullptr && c.live) {
+          load8(wt + c.lo, wa);
+          load8(wt + c.hi, wb);
         }
         float ss = 0.0f, gx = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           ss += xa[e] * xa[e] + xb[e] * xb[e];
-          gx += ga[e] * w[e] * xa[e] + gb[e] * w[8 + e] * xb[e];
+          gx += ga[e] * wa[e] * xa[e] + gb[e] * wb[e] * xb[e];
         }
         ss = sum_lanes<L>(ss);
         gx = sum_lanes<L>(gx);
@@ -401,12 +440,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float ha = xa[e] * rstd, hb = xb[e] * rstd;
           acc[k][e] += ga[e] * ha;
           acc[k][8 + e] += gb[e] * hb;
-          xa[e] = rstd * (ga[e] * w[e] - ha * m);
-          xb[e] = rstd * (gb[e] * w[8 + e] - hb * m);
+          xa[e] = rstd * (ga[e] * wa[e] - ha * m);
+          xb[e] = rstd * (gb[e] * wb[e] - hb * m);
         }
         if (live) {
           store8<E>(DX + off + c.lo, xa);
           store8<E>(DX + off + c.hi, xb);
+        }
+        if (more) {
+          if (sizeof(E) == 2)
+            cur = nxt;
+          else
+            fetch(base + ROWS + threadIdx.x / L, cur);
         }
       }
     }
@@ -524,25 +569,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// dw[k][e] = sum over CTAs of partial[cta][k][e]: 32 elements a CTA, 8 lanes
-// of rows, each lane in CTA order, then the lanes in order.
+// dw[k][e] = sum over CTAs of partial[cta][k][e]: 8 elements a CTA, 32 lanes of
+// rows, each lane in CTA order, then the lanes in order.
+constexpr int kFoldCols = 8, kFoldLanes = kThreads / kFoldCols;
 __global__ void __launch_bounds__(kThreads)
     fold_weight_grads_kernel(const float* __restrict__ partial, float* dwq, float* dwk, int32_t n,
                              int32_t dh) {
-  __shared__ float red[8][32];
+  __shared__ float red[kFoldLanes][kFoldCols];
   pdl_wait();
   pdl_launch_dependents();
-  const int32_t col = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32;
+  const int32_t col = blockIdx.x * kFoldCols + threadIdx.x % kFoldCols, lane = threadIdx.x / kFoldCols;
   float s = 0.0f;
   if (col < 2 * dh) {
-    for (int32_t i = lane; i < n; i += 8) s += partial[static_cast<int64_t>(i) * 2 * dh + col];
+#pragma unroll 8
+    for (int32_t i = lane; i < n; i += kFoldLanes) s += partial[static_cast<int64_t>(i) * 2 * dh + col];
   }
-  red[lane][threadIdx.x % 32] = s;
+  red[lane][threadIdx.x % kFoldCols] = s;
   __syncthreads();
   if (lane == 0 && col < 2 * dh) {
     s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x % 32];
+    for (int i = 0; i < kFoldLanes; ++i) s += red[i][threadIdx.x % kFoldCols];
     float* out = col < dh ? dwq : dwk;
     if (out != nullptr) out[col < dh ? col : col - dh] = s;
   }
@@ -633,7 +680,7 @@ cudaError_t launch_rope(const LaunchCtx& c, const RopeCall& a) {
   return e;
 }
 
-constexpr int kBwdCtas = 512;
+constexpr int kBwdCtas = 296;   // two an SM, all at once
 int64_t norm_rope_bwd_ctas(int64_t T) { return T < kBwdCtas ? (T > 0 ? T : 1) : kBwdCtas; }
 
 cudaError_t launch_norm_rope_bwd(const LaunchCtx& c, const RopeCall& a) {
@@ -645,7 +692,7 @@ cudaError_t launch_norm_rope_bwd(const LaunchCtx& c, const RopeCall& a) {
                                      : launch_backward<float>(c, a, P, grid);
   note_launch();
   if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
-  e = launch_pdl(fold_weight_grads_kernel, dim3(ceil_div(2 * a.dh, 32)), dim3(kThreads), 0, c.stream,
+  e = launch_pdl(fold_weight_grads_kernel, dim3(ceil_div(2 * a.dh, kFoldCols)), dim3(kThreads), 0, c.stream,
                  static_cast<const float*>(a.partial), a.dwq, a.dwk, static_cast<int32_t>(ctas),
                  static_cast<int32_t>(a.dh));
   note_launch();
