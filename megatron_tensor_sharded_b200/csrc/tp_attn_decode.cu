@@ -8,14 +8,17 @@
 // CTAs leaves one partial (max, sum, O) each, and decode_join_kernel adds them
 // in the order of the CTAs: the same bits on every run.
 //
-// A group's query heads (padded to the 16 rows of an MMA tile; more than 16
-// heads take several items that share their cache lines through L2) run
-// together, so the cache is read once for all of them.  Each of the four warps
-// has its own 16 keys of a tile and its own three-slot ring, filled by
-// 16-byte asynchronous copies, with its own running maximum: no barrier in
-// the loop.  The products are warp-level MMAs (m16n8k16): a tensor-core tile
-// of 128 rows would be nearly empty here, and the arithmetic is a tenth of
-// what the copies take.  Two CTAs an SM keep up to 192 KB in flight.
+// A group's query heads run together, so the cache is read once for all of
+// them: 8 or 16 to an item (more take several items that share their cache
+// lines through L2).  Each of the four warps has its own 16 keys of a tile and
+// its own three-slot ring, filled by 16-byte asynchronous copies, with its own
+// running maximum: no barrier in the loop.  The products are warp-level MMAs
+// (m16n8k16; a 128-row tensor-core tile would be nearly empty) of the
+// transposed tiles, S^T = K Q^T and O^T = V^T P^T, so that the cache fills the
+// MMA's 16 rows and the few heads its 8 columns: half the products and half
+// the softmax of the form with padded head rows, which was bound by its
+// instructions (735 a warp and tile; 79 us of 8192-token caches against 64 at
+// HBM's rate).  Two CTAs an SM keep up to 192 KB in flight.
 //
 // Keys behind a sequence's length are never read (their copies are zero
 // filled) and masked; the appended key and value come from the call's K_new
@@ -41,10 +44,11 @@ constexpr int DH = 128;
 constexpr int TILE = 64;                 // keys of a tile, 16 a warp
 constexpr int WARPS = 4;
 constexpr int NST = 3;                   // ring slots of a warp
-constexpr int MROWS = 16;                // query heads of an item
+constexpr int MROWS = 16;                // most query heads of an item
+constexpr int SUM_LD = DH + 4;           // floats between heads of the CTA's joined O
 constexpr int WTILE_BYTES = 16 * DH * 2; // a warp's keys (or values) of a tile
 constexpr int RING_BYTES = WARPS * NST * 2 * WTILE_BYTES;
-constexpr int SMEM_BYTES = RING_BYTES + MROWS * DH * 4 + 2 * WARPS * MROWS * 4;
+constexpr int SMEM_BYTES = RING_BYTES + MROWS * SUM_LD * 4 + 2 * WARPS * MROWS * 4;
 constexpr int CTAS_PER_SM = 2;
 constexpr int PART_FLOATS = MROWS * (DH + 2);   // O rows, then max and sum of each
 constexpr float kLog2e = 1.4426950408889634f;
@@ -55,7 +59,8 @@ struct DecodeParams {
   float *LSE, *part;
   const int32_t* len;
   const float* slopes;
-  int32_t B, p, hq, hkv, group, mtiles, heads, ctas;   // heads: items of a sequence
+  int32_t B, p, hq, hkv, group, rows, mtiles, heads, ctas;   // rows: heads of an item, 8 or 16;
+                                                             // heads: items of a sequence
   int64_t capacity;
   ScoreConsts s;
   unsigned* err;
@@ -127,6 +132,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 tile of bf16 held as fragments, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // 16-byte chunk c of row r of a warp's 16 x 256-byte tile, swizzled so that
 // eight rows' chunks of one column lie in different banks.
 __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
@@ -150,7 +161,8 @@ __device__ __forceinline__ void advance(const DecodeParams& P, Place& x) {
   } while (x.tiles == 0);
 }
 
-template <bool CAP, bool BIAS>
+// NT: 8-head column tiles of an item.
+template <bool CAP, bool BIAS, int NT>
 __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
     decode_kernel(const __grid_constant__ DecodeParams P) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -159,7 +171,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t ring = smem_u32(smem) + warp * NST * 2 * WTILE_BYTES;
   float* const sum_o = reinterpret_cast<float*>(smem + RING_BYTES);          // [16][128]
-  float* const warp_m = sum_o + MROWS * DH;                                  // [warp][16]
+  float* const warp_m = sum_o + MROWS * SUM_LD;                              // [warp][16]
   float* const warp_l = warp_m + WARPS * MROWS;
   pdl_wait();
   pdl_launch_dependents();
@@ -209,21 +221,33 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
       const int fresh = P.Kn != nullptr ? get.keys - 1 - static_cast<int>(key0) : -1;
       const int left = get.keys - static_cast<int>(key0);
       const uint32_t kt = ring + st * 2 * WTILE_BYTES, vt = kt + WTILE_BYTES;
-      const int c = lane % 16;
+      const int c = lane % 16, r0 = lane / 16;
+      if (left > 16 || (left == 16 && fresh < 0)) {   // cached rows only
+        const __nv_bfloat16* k = P.Kc + off + r0 * pitch + c * 8;
+        const __nv_bfloat16* v = P.Vc + off + r0 * pitch + c * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 2 + lane / 16;
-        const bool own = r == fresh, read = r < left;
-        // (an address in range also where nothing is read)
-        const int64_t src = own ? off_new : off + (read ? r : 0) * pitch;
-        const __nv_bfloat16* k = (own ? P.Kn : P.Kc) + src + c * 8;
-        const __nv_bfloat16* v = (own ? P.Vn : P.Vc) + src + c * 8;
-        cp_async16(chunk_at(kt, r, c), read ? k : P.Kc, read);
-        cp_async16(chunk_at(vt, r, c), read ? v : P.Vc, read);
-        if (own && get.h % P.mtiles == 0) {
-          const int64_t to = off + r * pitch + c * 8;
-          *reinterpret_cast<uint4*>(P.Kc + to) = *reinterpret_cast<const uint4*>(k);
-          *reinterpret_cast<uint4*>(P.Vc + to) = *reinterpret_cast<const uint4*>(v);
+        for (int i = 0; i < 8; ++i) {
+          cp_async16(chunk_at(kt, i * 2 + r0, c), k, true);
+          cp_async16(chunk_at(vt, i * 2 + r0, c), v, true);
+          k += 2 * pitch;
+          v += 2 * pitch;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 2 + r0;
+          const bool own = r == fresh, read = r < left;
+          // (an address in range also where nothing is read)
+          const int64_t src = own ? off_new : off + r * pitch;
+          const __nv_bfloat16* k = read ? (own ? P.Kn : P.Kc) + src + c * 8 : P.Kc;
+          const __nv_bfloat16* v = read ? (own ? P.Vn : P.Vc) + src + c * 8 : P.Vc;
+          cp_async16(chunk_at(kt, r, c), k, read);
+          cp_async16(chunk_at(vt, r, c), v, read);
+          if (own && get.h % P.mtiles == 0) {
+            const int64_t to = off + r * pitch + c * 8;
+            *reinterpret_cast<uint4*>(P.Kc + to) = *reinterpret_cast<const uint4*>(k);
+            *reinterpret_cast<uint4*>(P.Vc + to) = *reinterpret_cast<const uint4*>(v);
+          }
         }
       }
       advance(P, get);
@@ -234,8 +258,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
 #pragma unroll
   for (int st = 0; st < NST - 1; ++st) fetch(w0 + st, st);
 
-  uint32_t q[8][4];
-  float o[16][4], m[2], l[2], slope2[2];
+  // a thread's heads: columns 2 (lane % 4) and the next one of each 8-head tile
+  uint32_t q[NT][8][2];
+  float o[NT][8][4], m[NT][2], l[NT][2], slope2[NT][2];
   bool first = true;        // the item at hand began before this CTA
   bool open = false;        // q, o, m, l hold an item
   int slot = 0;
@@ -245,28 +270,28 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
       const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
       const __nv_bfloat16* Q =
           P.Q + ((static_cast<int64_t>(shard) * P.B + use.b) * P.hq + kvh * P.group) * DH;
-      const int r0 = mt * MROWS + lane / 4, r1 = r0 + 8;   // query heads of the group
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const int d = kk * 16 + (lane % 4) * 2;
-        const uint32_t* a = reinterpret_cast<const uint32_t*>(Q + static_cast<int64_t>(r0) * DH + d);
-        const uint32_t* b = reinterpret_cast<const uint32_t*>(Q + static_cast<int64_t>(r1) * DH + d);
-        q[kk][0] = r0 < P.group ? a[0] : 0u;
-        q[kk][1] = r1 < P.group ? b[0] : 0u;
-        q[kk][2] = r0 < P.group ? a[4] : 0u;
-        q[kk][3] = r1 < P.group ? b[4] : 0u;
+      for (int t = 0; t < NT; ++t) {
+        const int r = mt * P.rows + t * 8 + lane / 4;   // query head of the group
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(Q + static_cast<int64_t>(r) * DH) + lane % 4;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          q[t][kk][0] = r < P.group ? a[kk * 8] : 0u;
+          q[t][kk][1] = r < P.group ? a[kk * 8 + 4] : 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int rh = mt * P.rows + t * 8 + (lane % 4) * 2 + h;
+          if (BIAS)
+            slope2[t][h] = rh < P.group ? kLog2e * P.slopes[shard * P.hq + kvh * P.group + rh] : 0.0f;
+          m[t][h] = -INFINITY;
+          l[t][h] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
       }
-      if (BIAS) {
-        const float* sl = P.slopes + shard * P.hq + kvh * P.group;
-        slope2[0] = r0 < P.group ? kLog2e * sl[r0] : 0.0f;
-        slope2[1] = r1 < P.group ? kLog2e * sl[r1] : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.0f;
       open = true;
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
@@ -274,117 +299,124 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
     fetch(w + NST - 1, slot == 0 ? NST - 1 : slot - 1);   // the slot of the tile before this one
     const uint32_t kt = ring + slot * 2 * WTILE_BYTES, vt = kt + WTILE_BYTES;
 
-    // scores of 16 heads x 16 keys
-    float s[2][4] = {};
+    // scores of 16 keys x 8 heads a tile: keys lane / 4 and + 8 of a thread
+    float s[NT][4] = {};
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-      uint32_t k4[4];   // keys 0..7 / 8..15 by the two halves of 16 elements
-      ldsm4(k4, chunk_at(kt, (lane & 7) + ((lane >> 4) & 1) * 8, kk * 2 + ((lane >> 3) & 1)));
-      mma16816(s[0], q[kk], k4[0], k4[1]);
-      mma16816(s[1], q[kk], k4[2], k4[3]);
-    }
-    const int32_t key0 = static_cast<int32_t>(use.tile * TILE) + warp * 16;
-    float mx[2] = {-INFINITY, -INFINITY};
+      uint32_t k4[4];
+      ldsm4(k4, chunk_at(kt, (lane & 7) + ((lane >> 3) & 1) * 8, kk * 2 + (lane >> 4)));
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+      for (int t = 0; t < NT; ++t) mma16816(s[t], k4, q[t][kk][0], q[t][kk][1]);
+    }
+    const int32_t key0 = static_cast<int32_t>(use.tile * TILE) + warp * 16 + lane / 4;
+    const bool ends = key0 - lane / 4 + 16 > use.keys;   // (same for the warp)
+    float mx[NT][2];
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int32_t key = key0 + n * 8 + (lane % 4) * 2 + (e & 1);
         float z;
         if (CAP) {
-          const float t = 1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s[n][e]) * P.s.two_x));
-          z = P.s.cap_log2 * copysignf(t, s[n][e]);
-          if (s[n][e] != s[n][e]) z = s[n][e];
+          const float x = 1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s[t][e]) * P.s.two_x));
+          z = P.s.cap_log2 * copysignf(x, s[t][e]);
         } else {
-          z = s[n][e] * P.s.scale_log2;
+          z = s[t][e] * P.s.scale_log2;
         }
-        if (BIAS) z = fmaf(slope2[e >> 1], static_cast<float>(key - (use.keys - 1)), z);
-        if (key >= use.keys) z = -INFINITY;
-        s[n][e] = z;
-        mx[e >> 1] = max3_nan(mx[e >> 1], z, z);
+        const int32_t key = key0 + (e >> 1) * 8;
+        if (BIAS) z = fmaf(slope2[t][e & 1], static_cast<float>(key - (use.keys - 1)), z);
+        if (ends && key >= use.keys) z = -INFINITY;
+        s[t][e] = z;
       }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mx[h] = max3_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1), mx[h]);
-      mx[h] = max3_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2), mx[h]);
-    }
-    const bool grow = !(mx[0] <= m[0]) || !(mx[1] <= m[1]);
-    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float mn = max3_nan(m[h], mx[h], mx[h]);
-        const float alpha = mn == -INFINITY ? 1.0f : ex2(m[h] - mn);
-        m[h] = mn;
-        l[h] *= alpha;
+        float x = max3_nan(s[t][h], s[t][h + 2], s[t][h]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][2 * h] *= alpha;
-          o[i][2 * h + 1] *= alpha;
+        for (int d = 4; d < 32; d *= 2) x = max3_nan(x, __shfl_xor_sync(0xffffffffu, x, d), x);
+        mx[t][h] = x;
+        grow |= !(x <= m[t][h]);
+      }
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mn = max3_nan(m[t][h], mx[t][h], mx[t][h]);
+          const float alpha = mn == -INFINITY ? 1.0f : ex2(m[t][h] - mn);
+          m[t][h] = mn;
+          l[t][h] *= alpha;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[t][i][h] *= alpha;
+            o[t][i][2 + h] *= alpha;
+          }
         }
       }
     }
-    const float mo[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-    uint32_t pa[4];
+    uint32_t pb[NT][2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float e4[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        e4[e] = ex2(s[n][e] - mo[e >> 1]);
-        l[e >> 1] += e4[e];
-      }
-      pa[n * 2] = pack2(e4[0], e4[1]);
-      pa[n * 2 + 1] = pack2(e4[2], e4[3]);
+    for (int t = 0; t < NT; ++t) {
+      const float m0 = m[t][0] == -INFINITY ? 0.0f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.0f : m[t][1];
+      const float e0 = ex2(s[t][0] - m0), e1 = ex2(s[t][1] - m1);
+      const float e2 = ex2(s[t][2] - m0), e3 = ex2(s[t][3] - m1);
+      l[t][0] += e0 + e2;
+      l[t][1] += e1 + e3;
+      pb[t][0] = transpose8x8(pack2(e0, e1));   // [key][head] -> [head][key]
+      pb[t][1] = transpose8x8(pack2(e2, e3));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t v4[4];   // keys 0..7, 8..15 of elements 16i.., then of 16i + 8..
-      ldsm4_t(v4, chunk_at(vt, (lane & 7) + ((lane >> 3) & 1) * 8, i * 2 + ((lane >> 4) & 1)));
-      mma16816(o[2 * i], pa, v4[0], v4[1]);
-      mma16816(o[2 * i + 1], pa, v4[2], v4[3]);
+      uint32_t v4[4];   // 16 elements x 16 keys, transposed on the way
+      ldsm4_t(v4, chunk_at(vt, (lane & 7) + (lane >> 4) * 8, i * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma16816(o[t][i], v4, pb[t][0], pb[t][1]);
     }
     __syncwarp();   // every lane is done with the slot
     slot = slot + 1 == NST ? 0 : slot + 1;
 
     const bool item_ends = use.tile + 1 == use.tiles;
     if (item_ends || w + 1 == w1) {
-      // join the warps: rows' maxima and sums, then O warp by warp
+      // join the warps: heads' maxima and sums, then O warp by warp
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if (lane % 4 == 0) {
-          warp_m[warp * MROWS + h * 8 + lane / 4] = m[h];
-          warp_l[warp * MROWS + h * 8 + lane / 4] = l[h];
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], d);
+          if (lane < 4) {
+            warp_m[warp * MROWS + t * 8 + lane * 2 + h] = m[t][h];
+            warp_l[warp * MROWS + t * 8 + lane * 2 + h] = l[t][h];
+          }
         }
       }
       __syncthreads();
-      float M[2], f[2];
+      float f[NT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        M[h] = -INFINITY;
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) {
-          const float x = warp_m[i * MROWS + h * 8 + lane / 4];
-          M[h] = max3_nan(M[h], x, x);
+        for (int h = 0; h < 2; ++h) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < WARPS; ++i) {
+            const float x = warp_m[i * MROWS + t * 8 + (lane % 4) * 2 + h];
+            M = max3_nan(M, x, x);
+          }
+          f[t][h] = m[t][h] == -INFINITY ? 0.0f : ex2(m[t][h] - M);
         }
-        f[h] = m[h] == -INFINITY ? 0.0f : ex2(m[h] - M[h]);
       }
       for (int i = 0; i < WARPS; ++i) {
         if (warp == i) {
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
+          for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float2* at = reinterpret_cast<float2*>(sum_o + (h * 8 + lane / 4) * DH + n * 8 + (lane % 4) * 2);
-              float2 x = make_float2(o[n][2 * h] * f[h], o[n][2 * h + 1] * f[h]);
-              if (i > 0) {
-                const float2 y = *at;
-                x.x += y.x;
-                x.y += y.y;
+            for (int n = 0; n < 8; ++n) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float* at = sum_o + (t * 8 + (lane % 4) * 2 + (e & 1)) * SUM_LD + n * 16 + lane / 4 + (e >> 1) * 8;
+                const float x = o[t][n][e] * f[t][e & 1];
+                *at = i > 0 ? *at + x : x;
               }
-              *at = x;
             }
           }
         }
@@ -393,7 +425,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
       const int32_t hk = use.h / P.mtiles, mt = use.h - hk * P.mtiles;
       const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
       const bool whole = item_ends && !(first && start.tile != 0);
-      const int rows = min(MROWS, P.group - mt * MROWS);
+      const int rows = min(P.rows, P.group - mt * P.rows);
       float* const part =
           P.part + (static_cast<int64_t>(blockIdx.x) * 2 + (first ? 0 : 1)) * PART_FLOATS;
       for (int row = warp; row < rows; row += WARPS) {
@@ -408,9 +440,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
           const float x = warp_m[i * MROWS + row];
           if (x != -INFINITY) L += warp_l[i * MROWS + row] * ex2(x - Mr);
         }
-        const float4 x = *reinterpret_cast<const float4*>(sum_o + row * DH + lane * 4);
+        const float4 x = *reinterpret_cast<const float4*>(sum_o + row * SUM_LD + lane * 4);
         if (whole) {
-          const int32_t head = kvh * P.group + mt * MROWS + row;
+          const int32_t head = kvh * P.group + mt * P.rows + row;
           const float inv = L == 0.0f ? 0.0f : 1.0f / L;
           *reinterpret_cast<uint2*>(
               P.O + ((static_cast<int64_t>(shard) * P.B + use.b) * P.hq + head) * DH + lane * 4) =
@@ -447,7 +479,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   const int32_t b = item / P.heads, h = item - b * P.heads;
   const int32_t hk = h / P.mtiles, mt = h - hk * P.mtiles;
   const int32_t shard = hk / P.hkv, kvh = hk - shard * P.hkv;
-  const int32_t in_group = mt * MROWS + blockIdx.y;
+  const int32_t in_group = mt * P.rows + blockIdx.y;
   if (in_group >= P.group) return;
   // The lengths were complete before the decode kernel, which this one waits
   // for, let it start: where the parts lie is worked out beside it.
@@ -522,7 +554,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   }
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, int NT>
 tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
   static uint64_t attr_epoch[64] = {};
   static std::mutex mu;
@@ -530,7 +562,7 @@ tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
     std::lock_guard<std::mutex> lk(mu);
     const int dev = c.device & 63;
     if (attr_epoch[dev] != c.epoch) {
-      if (cudaFuncSetAttribute(decode_kernel<CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(decode_kernel<CAP, BIAS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                SMEM_BYTES) != cudaSuccess) {
         set_error_detail("cudaFuncSetAttribute failed: %s", cudaGetErrorString(cudaGetLastError()));
         return TP_ERR_CUDA;
@@ -538,11 +570,11 @@ tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
       attr_epoch[dev] = c.epoch;
     }
   }
-  cudaError_t e = launch_pdl(decode_kernel<CAP, BIAS>, dim3(prm.ctas), dim3(WARPS * 32), SMEM_BYTES,
+  cudaError_t e = launch_pdl(decode_kernel<CAP, BIAS, NT>, dim3(prm.ctas), dim3(WARPS * 32), SMEM_BYTES,
                              c.stream, prm);
   note_launch();
   if (e == cudaSuccess) {
-    e = launch_pdl(decode_join_kernel, dim3(prm.B * prm.heads, prm.group < MROWS ? prm.group : MROWS),
+    e = launch_pdl(decode_join_kernel, dim3(prm.B * prm.heads, prm.group < prm.rows ? prm.group : prm.rows),
                    dim3(JOIN_THREADS), 0, c.stream, prm);
     note_launch();
   }
@@ -555,10 +587,13 @@ tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
 
 }  // namespace
 
+// Query heads of an item: 8 where one column tile holds the group.
+int item_rows(int group) { return group <= 8 ? 8 : MROWS; }
+
 // CTAs that share the line of tiles: two an SM, fewer where the caches could
 // not give each a tile.
 int64_t decode_ctas(int num_sms, int64_t B, int64_t capacity, int p, int hq, int hkv) {
-  const int64_t mtiles = (hq / hkv + MROWS - 1) / MROWS;
+  const int64_t mtiles = (hq / hkv + item_rows(hq / hkv) - 1) / item_rows(hq / hkv);
   const int64_t most = B * p * hkv * mtiles * ((capacity + TILE - 1) / TILE);
   int64_t full = static_cast<int64_t>(num_sms) * CTAS_PER_SM;
   if (full > kMaxDecodeCtas) full = kMaxDecodeCtas;
@@ -585,17 +620,24 @@ tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a) {
   prm.hq = a.hq;
   prm.hkv = a.hkv;
   prm.group = a.hq / a.hkv;
-  prm.mtiles = (prm.group + MROWS - 1) / MROWS;
+  prm.rows = item_rows(prm.group);
+  prm.mtiles = (prm.group + prm.rows - 1) / prm.rows;
   prm.heads = a.p * a.hkv * prm.mtiles;
   prm.capacity = a.capacity;
   prm.s = score_consts(a.scale, a.cap);
   prm.err = c.err_word;
   prm.ctas = static_cast<int32_t>(decode_ctas(c.num_sms, a.B, a.capacity, a.p, a.hq, a.hkv));
   const bool cap = a.cap > 0.0f, bias = a.slopes != nullptr;
-  if (cap && bias) return launch_decode<true, true>(c, prm);
-  if (cap) return launch_decode<true, false>(c, prm);
-  if (bias) return launch_decode<false, true>(c, prm);
-  return launch_decode<false, false>(c, prm);
+  if (prm.rows == 8) {
+    if (cap && bias) return launch_decode<true, true, 1>(c, prm);
+    if (cap) return launch_decode<true, false, 1>(c, prm);
+    if (bias) return launch_decode<false, true, 1>(c, prm);
+    return launch_decode<false, false, 1>(c, prm);
+  }
+  if (cap && bias) return launch_decode<true, true, 2>(c, prm);
+  if (cap) return launch_decode<true, false, 2>(c, prm);
+  if (bias) return launch_decode<false, true, 2>(c, prm);
+  return launch_decode<false, false, 2>(c, prm);
 }
 
 }  // namespace tpk

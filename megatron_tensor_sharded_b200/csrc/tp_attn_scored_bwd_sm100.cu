@@ -257,9 +257,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int o = 8; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (row < rows && lane == 0) {
-      const int64_t st = row / hq;            // shard * T + t
-      const int64_t shard = st / T;
-      delta[(shard * hq + row % hq) * T + (st - shard * T)] = s;
+      int64_t st, shard;   // st = shard * T + t
+      if (rows >> 31) {
+        st = row / hq;
+        shard = st / T;
+      } else {
+        st = static_cast<uint32_t>(row) / static_cast<uint32_t>(hq);
+        shard = static_cast<uint32_t>(st) / static_cast<uint32_t>(T);
+      }
+      delta[(shard * hq + (row - st * hq)) * T + (st - shard * T)] = s;
     }
   }
 }

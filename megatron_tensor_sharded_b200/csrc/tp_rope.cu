@@ -43,6 +43,22 @@ constexpr int kMaxHead = 256;
 constexpr int kMaxPairs = kMaxHead / 2;
 constexpr int kMaxTok = 4;   // tokens a CTA takes at once
 
+// n / d for 0 <= n < 2^31 by a multiplication (the round-up method: m =
+// floor(2^32 (2^s - d) / d) + 1 with s the bits of d - 1).
+struct FastDiv {
+  uint32_t m;
+  int32_t s, d;
+  FastDiv() = default;
+  explicit FastDiv(int32_t div) : d(div < 1 ? 1 : div) {
+    s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int32_t div(int32_t n) const {
+    return static_cast<int32_t>((__umulhi(m, static_cast<uint32_t>(n)) + static_cast<uint32_t>(n)) >> s);
+  }
+};
+
 struct RopeParams {
   const void *Q, *K, *dYq, *dYk;   // K (and Q) may be null with 0 rows a token
   void *Qo, *Ko;
@@ -52,7 +68,8 @@ struct RopeParams {
   int32_t T, p, hq, hk, dh, r2;    // heads per shard; r2 rotated pairs
   int32_t tok, row_split;          // tokens a CTA, rows of a token a CTA
   int32_t interleaved;
-  float eps, amp, sign;            // sign -1: rotate back
+  FastDiv by_hq, by_hk;
+  float eps, inv_dh, amp, sign;    // sign -1: rotate back
   uint64_t turn[kMaxPairs];        // fraction of a turn per position, 2^-64 units
 };
 
@@ -129,10 +146,10 @@ __device__ __forceinline__ void fill_angles(const RopeParams& P, int32_t t0, int
   }
 }
 
-// Offset of row w of token t in its tensor (h heads a shard): rows go shard by
-// shard, head by head.
-__device__ __forceinline__ int64_t row_offset(const RopeParams& P, int32_t t, int32_t w, int32_t h) {
-  const int32_t shard = w / h, head = w - shard * h;
+// Offset of row w of token t in Q or K: rows go shard by shard, head by head.
+__device__ __forceinline__ int64_t row_offset(const RopeParams& P, int32_t t, int32_t w, bool k) {
+  const int32_t h = k ? P.hk : P.hq;
+  const int32_t shard = k ? P.by_hk.div(w) : P.by_hq.div(w), head = w - shard * h;
   return ((static_cast<int64_t>(shard) * P.T + t) * h + head) * P.dh;
 }
 
@@ -152,11 +169,8 @@ __device__ __forceinline__ Chunk chunk_of(const RopeParams& P, int32_t u) {
   return c;
 }
 
-__device__ __forceinline__ void rotate(const float* cs, const float* sn, bool interleaved,
+__device__ __forceinline__ void rotate(const float (&c)[8], const float (&s)[8], bool interleaved,
                                        float (&a)[8], float (&b)[8]) {
-  float c[8], s[8];
-  load8(cs, c);
-  load8(sn, s);
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -195,37 +209,45 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
   const int32_t t0 = blockIdx.x * P.tok;
   const int32_t ntok = min(P.tok, P.T - t0);
   const int32_t qrows = P.p * P.hq, rows = qrows + P.p * P.hk;
-  const int32_t w0 = blockIdx.y * P.row_split, nw = min(P.row_split, rows - w0);
-  const int32_t total = ntok * nw;
+  const int32_t w0 = blockIdx.y * P.row_split, w1 = w0 + min(P.row_split, rows - w0);
   const Chunk c = chunk_of(P, threadIdx.x % L);
-  // BATCH rows of a thread are loaded together (enough bytes in flight to
-  // cover the latency of HBM), the first ones before the angles are computed
-  constexpr int BATCH = sizeof(E) == 2 ? 4 : 2;
-  for (int32_t base = 0; base < total; base += BATCH * ROWS) {
+  // A thread keeps its token and its pairs, so its sines and cosines stay in
+  // registers; it takes every (ROWS / tok)-th of the token's heads.  BATCH of
+  // them are loaded together (bytes in flight against HBM's latency), the
+  // first ones before the angles are computed.
+  const int32_t per = ROWS / P.tok, slot = threadIdx.x / L;
+  const int32_t tl = slot / per, t = t0 + tl;
+  const bool live = tl < ntok && c.live;
+  constexpr int BATCH = sizeof(E) == 2 ? 3 : 2;
+  float cv[8], sv[8];
+  const int32_t steps = (w1 - w0 + per - 1) / per;
+  for (int32_t step = 0; step < steps; step += BATCH) {
     Raw8<E> ra[BATCH], rb[BATCH];
     int64_t off[BATCH];
-    int32_t tl[BATCH];
     bool isk[BATCH];
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
-      const int32_t i = base + n * ROWS + threadIdx.x / L;
-      const bool in = i < total && c.live;
-      tl[n] = in ? i / nw : 0;
-      int32_t w = in ? w0 + i - tl[n] * nw : 0;
+      int32_t w = w0 + slot - tl * per + (step + n) * per;
+      const bool in = live && w < w1;
       isk[n] = w >= qrows;
       if (isk[n]) w -= qrows;
-      off[n] = in ? row_offset(P, t0 + tl[n], w, isk[n] ? P.hk : P.hq) : -1;
+      off[n] = -1;
       ra[n].zero();
       rb[n].zero();
       if (in) {
+        off[n] = row_offset(P, t, w, isk[n]);
         const E* src = static_cast<const E*>(isk[n] ? P.K : P.Q) + off[n];
         ra[n].load(src + c.lo);
         rb[n].load(src + c.hi);
       }
     }
-    if (base == 0) {
+    if (step == 0) {
       fill_angles(P, t0, ntok, cs, sn);
       __syncthreads();
+      if (c.turn && live) {
+        load8(cs + tl * kMaxPairs + c.pair0, cv);
+        load8(sn + tl * kMaxPairs + c.pair0, sv);
+      }
     }
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
@@ -237,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss += va[e] * va[e] + vb[e] * vb[e];
         ss = sum_lanes<L>(ss);
-        const float rstd = rsqrtf(ss / static_cast<float>(P.dh) + P.eps);
+        const float rstd = rsqrtf(ss * P.inv_dh + P.eps);
         const float* w = isk[n] ? P.wk : P.wq;
         if (w != nullptr && c.live) {
           float wl[8], wh[8];
@@ -256,9 +278,7 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
           }
         }
       }
-      if (c.turn)
-        rotate(cs + tl[n] * kMaxPairs + c.pair0, sn + tl[n] * kMaxPairs + c.pair0, P.interleaved, va,
-               vb);
+      if (c.turn) rotate(cv, sv, P.interleaved, va, vb);
       if (off[n] >= 0) {
         E* dst = static_cast<E*>(isk[n] ? P.Ko : P.Qo) + off[n];
         store8<E>(dst + c.lo, va);
@@ -304,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
     int32_t w = w0 + i - tl * nw;
     const bool k = w >= qrows;
     if (k) w -= qrows;
-    const int64_t off = row_offset(P, t0 + tl, w, k ? P.hk : P.hq);
+    const int64_t off = row_offset(P, t0 + tl, w, k);
     const E* src = static_cast<const E*>(k ? P.K : P.Q) + off;
     E* dst = static_cast<E*>(k ? P.Ko : P.Qo) + off;
     const float* wt = k ? P.wk : P.wq;
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constan
       }
     }
     float rstd = 1.0f;
-    if (NORM) rstd = rsqrtf(sum_lanes<32>(ss) / static_cast<float>(P.dh) + P.eps);
+    if (NORM) rstd = rsqrtf(sum_lanes<32>(ss) * P.inv_dh + P.eps);
 #pragma unroll
     for (int n = 0; n < kSlots; ++n) {
       const int32_t s = lane + 32 * n;
@@ -362,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_launch_dependents();
   const int32_t u = threadIdx.x % L;
   const Chunk c = chunk_of(P, u);
+  const int32_t per = ROWS / P.tok;   // a thread keeps its token of the CTA's and takes every per-th head
+  const int32_t tl = static_cast<int32_t>(threadIdx.x) / L / per, lane_row = threadIdx.x / L - tl * per;
   float acc[2][16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = 0.0f;
@@ -374,21 +396,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       const E* DY = static_cast<const E*>(k ? P.dYk : P.dYq);
       E* DX = static_cast<E*>(k ? P.Ko : P.Qo);
       const float* wt = k ? P.wk : P.wq;
-      const int32_t total = ntok * nw;
       struct Row {
         Raw8<E> xa, xb, ga, gb;
         int64_t off;
-        int32_t tl;
       };
-      auto fetch = [&](int32_t i, Row& r) {
-        const bool in = i < total && c.live;
-        r.tl = in ? i / nw : 0;
-        r.off = in ? row_offset(P, t0 + r.tl, i - r.tl * nw, h) : -1;
+      auto fetch = [&](int32_t w, Row& r) {
+        const bool in = tl < ntok && w < nw && c.live;
+        r.off = -1;
         r.xa.zero();
         r.xb.zero();
         r.ga.zero();
         r.gb.zero();
         if (in) {
+          r.off = row_offset(P, t0 + tl, w, k != 0);
           r.xa.load(X + r.off + c.lo);
           r.xb.load(X + r.off + c.hi);
           r.ga.load(DY + r.off + c.lo);
@@ -396,17 +416,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       };
       Row cur;
-      fetch(threadIdx.x / L, cur);
+      fetch(lane_row, cur);
       if (k == 0) {   // (the first rows are on their way)
         __syncthreads();   // the angles of the previous tokens are no longer read
         fill_angles(P, t0, ntok, cs, sn);
         __syncthreads();
       }
-      for (int32_t base = 0; base < total; base += ROWS) {
+      for (int32_t base = 0; base < nw; base += per) {
         Row nxt;
         // (fp32 rows take twice the registers: loaded where they are used)
-        const bool more = base + ROWS < total;
-        if (sizeof(E) == 2 && more) fetch(base + ROWS + threadIdx.x / L, nxt);
+        const bool more = base + per < nw;
+        if (sizeof(E) == 2 && more) fetch(base + per + lane_row, nxt);
         const bool live = cur.off >= 0;
         const int64_t off = cur.off;
         float xa[8], xb[8], ga[8], gb[8];
@@ -414,9 +434,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         cur.xb.get(xb);
         cur.ga.get(ga);
         cur.gb.get(gb);
-        if (c.turn)
-          rotate(cs + cur.tl * kMaxPairs + c.pair0, sn + cur.tl * kMaxPairs + c.pair0,
-                 P.interleaved, ga, gb);
+        if (c.turn) {
+          float cv[8], sv[8];
+          load8(cs + tl * kMaxPairs + c.pair0, cv);
+          load8(sn + tl * kMaxPairs + c.pair0, sv);
+          rotate(cv, sv, P.interleaved, ga, gb);
+        }
         float wa[8], wb[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
@@ -432,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         ss = sum_lanes<L>(ss);
         gx = sum_lanes<L>(gx);
-        const float inv_dh = 1.0f / static_cast<float>(P.dh);
+        const float inv_dh = P.inv_dh;
         const float rstd = rsqrtf(ss * inv_dh + P.eps);
         const float m = gx * rstd * inv_dh;   // mean(g w xhat)
 #pragma unroll
@@ -451,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (sizeof(E) == 2)
             cur = nxt;
           else
-            fetch(base + ROWS + threadIdx.x / L, cur);
+            fetch(base + per + lane_row, cur);
         }
       }
     }
@@ -509,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       for (int32_t i = warp; i < ntok * nw; i += kThreads / 32) {
         const int32_t tl = i / nw;
-        const int64_t off = row_offset(P, t0 + tl, i - tl * nw, h);
+        const int64_t off = row_offset(P, t0 + tl, i - tl * nw, k != 0);
         float x[kSlots][2], g[kSlots][2], ss = 0.0f, gx = 0.0f;
 #pragma unroll
         for (int n = 0; n < kSlots; ++n) {
@@ -534,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         ss = sum_lanes<32>(ss);
         gx = sum_lanes<32>(gx);
-        const float inv_dh = 1.0f / static_cast<float>(P.dh);
+        const float inv_dh = P.inv_dh;
         const float rstd = rsqrtf(ss * inv_dh + P.eps);
         const float m = gx * rstd * inv_dh;
 #pragma unroll
@@ -620,6 +643,9 @@ RopeParams params_of(const RopeCall& a) {
   P.hq = a.hq;
   P.hk = a.hk;
   P.dh = a.dh;
+  P.by_hq = FastDiv(a.hq);
+  P.by_hk = FastDiv(a.hk);
+  P.inv_dh = 1.0f / static_cast<float>(a.dh);
   P.eps = a.eps;
   P.amp = 1.0f;
   P.sign = a.back ? -1.0f : 1.0f;
@@ -686,7 +712,8 @@ int64_t norm_rope_bwd_ctas(int64_t T) { return T < kBwdCtas ? (T > 0 ? T : 1) : 
 cudaError_t launch_norm_rope_bwd(const LaunchCtx& c, const RopeCall& a) {
   RopeParams P = params_of(a);
   const int64_t ctas = norm_rope_bwd_ctas(a.T);
-  P.tok = a.T >= ctas * kMaxTok ? kMaxTok : ceil_div(a.T, ctas);
+  // tokens a CTA takes at once: a power of two, since they share its row slots
+  P.tok = a.T >= ctas * 4 ? 4 : a.T >= ctas * 2 ? 2 : 1;
   const dim3 grid(static_cast<unsigned>(ctas));
   cudaError_t e = a.dtype == TP_BF16 ? launch_backward<__nv_bfloat16>(c, a, P, grid)
                                      : launch_backward<float>(c, a, P, grid);
