@@ -514,23 +514,40 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   if (c0 == c1) return;   // written whole
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int64_t c = c0 + warp; c <= c1; c += JOIN_THREADS / 32) {
-    const int64_t first = share_of(total, c, P.ctas);
-    if (first == share_of(total, c + 1, P.ctas)) continue;   // fewer tiles than CTAs
-    // a CTA's first item is its slot 0; the item begins inside c0 unless it
-    // begins with it
-    const bool second = c == c0 && first != a;
-    const float* part = P.part + (c * 2 + (second ? 1 : 0)) * PART_FLOATS;
-    const float pm = part[MROWS * DH + blockIdx.y], pl = part[MROWS * DH + MROWS + blockIdx.y];
-    const float4 x = *reinterpret_cast<const float4*>(part + blockIdx.y * DH + lane * 4);
-    const float mn = max3_nan(m, pm, pm);
-    const float fa = m == -INFINITY ? 0.0f : ex2(m - mn), fb = pm == -INFINITY ? 0.0f : ex2(pm - mn);
-    l = l * fa + pl * fb;
-    o.x = o.x * fa + x.x * fb;
-    o.y = o.y * fa + x.y * fb;
-    o.z = o.z * fa + x.z * fb;
-    o.w = o.w * fa + x.w * fb;
-    m = mn;
+  constexpr int GROUPS = JOIN_THREADS / 32, AHEAD = 4;   // parts of a warp loaded together
+  for (int64_t cb = c0 + warp; cb <= c1; cb += GROUPS * AHEAD) {
+    float pm[AHEAD], pl[AHEAD];
+    float4 x[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int64_t c = cb + i * GROUPS;
+      pm[i] = -INFINITY;
+      pl[i] = 0.0f;
+      x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int64_t first = share_of(total, c, P.ctas);
+      // (a CTA without a tile, where there are fewer tiles than CTAs, left none)
+      if (c <= c1 && first < share_of(total, c + 1, P.ctas)) {
+        // a CTA's first item is its slot 0; the item begins inside c0 unless it
+        // begins with it
+        const bool second = c == c0 && first != a;
+        const float* part = P.part + (c * 2 + (second ? 1 : 0)) * PART_FLOATS;
+        pm[i] = part[MROWS * DH + blockIdx.y];
+        pl[i] = part[MROWS * DH + MROWS + blockIdx.y];
+        x[i] = *reinterpret_cast<const float4*>(part + blockIdx.y * DH + lane * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const float mn = max3_nan(m, pm[i], pm[i]);
+      const float fa = m == -INFINITY ? 0.0f : ex2(m - mn);
+      const float fb = pm[i] == -INFINITY ? 0.0f : ex2(pm[i] - mn);
+      l = l * fa + pl[i] * fb;
+      o.x = o.x * fa + x[i].x * fb;
+      o.y = o.y * fa + x[i].y * fb;
+      o.z = o.z * fa + x[i].z * fb;
+      o.w = o.w * fa + x[i].w * fb;
+      m = mn;
+    }
   }
   if (lane == 0) {
     grp_m[warp] = m;

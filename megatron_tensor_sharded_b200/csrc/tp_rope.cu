@@ -200,7 +200,7 @@ __device__ __forceinline__ float sum_lanes(float v) {
 
 // ------------------------------------------------------------------ forward
 template <typename E, int L, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(kThreads, 3) rope_vec_kernel(const __grid_constant__ RopeParams P) {
   __shared__ __align__(16) float cs[kMaxTok * kMaxPairs];
   __shared__ __align__(16) float sn[kMaxTok * kMaxPairs];
   constexpr int ROWS = kThreads / L;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
   const int32_t per = ROWS / P.tok, slot = threadIdx.x / L;
   const int32_t tl = slot / per, t = t0 + tl;
   const bool live = tl < ntok && c.live;
-  constexpr int BATCH = sizeof(E) == 2 ? 3 : 2;
+  constexpr int BATCH = sizeof(E) == 2 && !NORM ? 3 : 2;
   float cv[8], sv[8];
   const int32_t steps = (w1 - w0 + per - 1) / per;
   for (int32_t step = 0; step < steps; step += BATCH) {
