@@ -7,13 +7,30 @@
 //   LSE_i = log sum_j exp z_ij.
 //
 // Bound by the tensor cores (4 * 128 flops a visible pair) and, with the cap,
-// by the softmax's arithmetic beside them.  The pipeline is that of
-// tc_attn_kernel: a unit is a (shard, query head, pair of 128-row query
-// tiles), K/V blocks of 128 keys go through a two-slot ring and feed both
-// tiles, scores and probabilities stay in TMEM (P over the scores it came
-// from), O accumulates in TMEM.  Roles (384 threads): warp 0 TMA, warp 1 MMA,
-// warps 2..3 look at V where a mask cuts a block, warps 4..7 and 8..11 the
-// softmax of one tile each, a thread a row.
+// by the softmax's arithmetic beside them.  A unit is a (shard, query head,
+// tile of 128 query rows); it walks blocks of 128 keys.  Sixteen warps do the
+// softmax (a thread is a row and half of a block's columns: 64 scores) in two
+// groups that take alternate blocks, so one group's waits and round trips to
+// TMEM are covered by the other's arithmetic; three score buffers in TMEM let
+// the tensor core run Q K^T up to three blocks ahead of P V.  (The form with
+// two query tiles that share the K/V blocks, each with one score buffer,
+// waited for the next scores after every block: 2780 clocks a tile and block
+// with the cap, of 1040 of products.)  The probabilities stay in TMEM, over
+// the scores they came from, as the A operand of P V.  A tensor-core
+// instruction is issued only when the pipe takes it, so whatever else the
+// issuing thread does adds to the products' time (90 clocks for a commit and a
+// wait after eight of them): Q K^T and P V have a thread each, and one's waits
+// run beside the other's products.
+// Roles (640 threads): warp 0 loads Q, K (two slots) and V (three), warp 1
+// issues Q K^T, warp 3 P V, warp 2 looks at V where a mask cuts a block, warps
+// 4..11 and 12..19 are the two softmax groups.
+//
+// Running maximum (shared by a row's four threads): block by block, each
+// group takes over the other's value as soon as it has its block's own
+// maximum, moves it only when it grows by more than 2^8, and hands it on
+// before its exponentials.  A group's sum follows when it next sees a larger
+// maximum; sums and O meet at the unit's end, which each group does after its
+// first block of the next unit.
 //
 // Blocks: each tile walks only the blocks between its rows' least and
 // greatest visible key (from the mask's plan; arithmetic without one), and
@@ -30,7 +47,7 @@
 //
 // A key that a row does not see adds nothing to it, whatever K and V hold
 // there: its score is replaced by -inf before the softmax, and where a mask
-// cuts a block warps 2..3 zero the rows of V that hold an infinity or NaN
+// cuts a block warp 2 zeroes the rows of V that hold an infinity or NaN
 // before P V reads them (0 * NaN would be NaN).  Rows that do see such a key
 // are made NaN through its bit in `bad`.
 #include <cuda.h>
@@ -56,23 +73,27 @@ namespace {
 constexpr int DH = 128;
 constexpr int BQ = kAttnTile;
 constexpr int BKV = kAttnTile;
-constexpr int NQT = 2;                       // query tiles per unit
-constexpr int NST = 2;                       // K/V ring slots
+constexpr int NK = 2;                        // ring slots of K
+constexpr int NV = 3;                        // ring slots of V
+constexpr int NS = 3;                        // score buffers in TMEM
 constexpr int TILE_BYTES = 128 * 128 * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;
-constexpr int XCH_BYTES = NQT * 2 * 2 * BQ * 4;   // [tile][parity][column half][row]
-constexpr int SMEM_BYTES = 1024 + NQT * TILE_BYTES + NST * 2 * TILE_BYTES + XCH_BYTES + 512;
+constexpr int TILES_BYTES = (1 + NK + NV) * TILE_BYTES;
+// floats: [group][half][row] maxima, [group][row] running maximum, and
+// [unit parity][sum, maximum, mark][part][row] for the unit's end
+constexpr int XCH_FLOATS = 2 * 2 * BQ + 2 * BQ + 2 * 3 * 4 * BQ;
+constexpr int SMEM_BYTES = 1024 + TILES_BYTES + XCH_FLOATS * 4 + 512;
 constexpr int NUM_THREADS = 640;
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BQ, BKV, 0, 0);
 constexpr uint32_t IDESC_O = idesc_bf16_f32(BQ, DH, 0, 1);
-constexpr uint32_t O_COL0 = NQT * BKV, TMEM_COLS = 512;
+constexpr uint32_t O_COL0 = NS * BKV, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float kBoundLog2 = 80.0f;          // |z| in log2 that needs no running maximum
 
 enum { kPlain = 0, kBias = 1, kCap = 2, kCapAny = 3 };   // kCap: no bias, bounded
 
 struct ScoredParams {
-  int32_t T, p, hq, hkv, group, q_blocks, q_pairs, num_units, causal;
+  int32_t T, p, hq, hkv, group, q_blocks, num_units, causal;
   MaskPlan mask;
   ScoreConsts s;
   const float* slopes;
@@ -83,38 +104,19 @@ struct ScoredParams {
 };
 
 struct Unit {
-  int32_t shard, head, kvh, qb0;
-  TileSpan t[NQT];
-  int32_t jmin, jmax;
-  // (selected, not indexed: the softmax warps' tile is a run-time number)
-  __device__ __forceinline__ TileSpan span(int i) const { return i == 0 ? t[0] : t[1]; }
-  __device__ __forceinline__ bool active(int i, int32_t j) const {
-    const TileSpan s = span(i);
-    return j >= s.jb && j < s.je;
-  }
-  __device__ __forceinline__ bool any(int i) const {
-    const TileSpan s = span(i);
-    return s.je > s.jb;
-  }
-  // block j holds a key that some row of an active tile does not see
-  __device__ __forceinline__ bool cut(int32_t j) const {
-    return (active(0, j) && !t[0].whole(j)) || (active(1, j) && !t[1].whole(j));
-  }
+  int32_t shard, head, kvh, qb;
+  TileSpan t;
 };
 
 __device__ __forceinline__ Unit decode_unit(const ScoredParams& P, int32_t u) {
   Unit x;
   const int32_t heads = P.p * P.hq;
-  const int32_t level = u / heads, hh = u % heads;
-  const int32_t qp = P.q_pairs - 1 - level;   // causal: the longest first
+  const int32_t level = u / heads, hh = u - level * heads;
+  x.qb = P.q_blocks - 1 - level;   // causal: the longest first
   x.shard = hh / P.hq;
-  x.head = hh % P.hq;
+  x.head = hh - x.shard * P.hq;
   x.kvh = x.head / P.group;
-  x.qb0 = qp * NQT;
-#pragma unroll
-  for (int i = 0; i < NQT; ++i) x.t[i] = tile_span(P.mask, x.qb0 + i, P.q_blocks, P.T, P.causal);
-  x.jmin = x.any(0) ? (x.any(1) ? min(x.t[0].jb, x.t[1].jb) : x.t[0].jb) : x.t[1].jb;
-  x.jmax = x.any(0) ? (x.any(1) ? max(x.t[0].je, x.t[1].je) : x.t[0].je) : x.t[1].je;
+  x.t = tile_span(P.mask, x.qb, P.q_blocks, P.T, P.causal);
   return x;
 }
 
@@ -123,6 +125,41 @@ __device__ __forceinline__ int32_t unit_of(int32_t r) {
   const int32_t g = static_cast<int32_t>(gridDim.x), b = static_cast<int32_t>(blockIdx.x);
   return r * g + ((r & 1) ? g - 1 - b : b);
 }
+
+// A walk over the blocks of the CTA's units (units without a block left out).
+struct Walk {
+  Unit x;
+  int32_t r, u, j;   // round, unit, block
+  uint32_t n, nu;    // blocks and units before this one
+  bool first, done;  // the unit's first block; the walk is over
+  __device__ __forceinline__ void find(const ScoredParams& P) {
+    for (; u < P.num_units; u = unit_of(++r)) {
+      x = decode_unit(P, u);
+      if (x.t.jb < x.t.je) {
+        j = x.t.jb;
+        first = true;
+        return;
+      }
+    }
+    done = true;
+  }
+  __device__ __forceinline__ void begin(const ScoredParams& P) {
+    r = 0;
+    u = unit_of(0);
+    n = nu = 0;
+    done = false;
+    find(P);
+  }
+  __device__ __forceinline__ bool last() const { return j + 1 == x.t.je; }
+  __device__ __forceinline__ void next(const ScoredParams& P) {
+    ++n;
+    first = false;
+    if (++j < x.t.je) return;
+    ++nu;
+    u = unit_of(++r);
+    find(P);
+  }
+};
 
 // Of every eight pairs of probabilities, those whose 2^x runs as a polynomial
 // on the FMA pipe, so that it and the MUFU unit (16 a clock and SM) are busy
@@ -182,45 +219,57 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  auto sQ = [&](uint32_t t) { return base + t * TILE_BYTES; };
-  auto sK = [&](uint32_t st) { return base + NQT * TILE_BYTES + st * 2 * TILE_BYTES; };
-  auto sV = [&](uint32_t st) { return sK(st) + TILE_BYTES; };
-  constexpr int RING_END = NQT * TILE_BYTES + NST * 2 * TILE_BYTES;
-  volatile float* const xch = reinterpret_cast<volatile float*>(smem_raw + (base - raw) + RING_END);
-  uint8_t* const ctrl = smem_raw + (base - raw) + RING_END + XCH_BYTES;
+  const uint32_t sQ = base;
+  auto sK = [&](uint32_t n) { return base + (1 + n % NK) * TILE_BYTES; };
+  auto sV = [&](uint32_t n) { return base + (1 + NK + n % NV) * TILE_BYTES; };
+  volatile float* const xch = reinterpret_cast<volatile float*>(smem_raw + (base - raw) + TILES_BYTES);
+  volatile float* const run_m = xch + 2 * 2 * BQ;
+  volatile float* const ends = run_m + 2 * BQ;
+  uint8_t* const ctrl = smem_raw + (base - raw) + TILES_BYTES + XCH_FLOATS * 4;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ctrl);
-  const uint32_t q_full = smem_u32(&bars[0]), q_empty = smem_u32(&bars[1]);
-  auto kv_full = [&](uint32_t s) { return smem_u32(&bars[2 + s]); };
-  auto kv_empty = [&](uint32_t s) { return smem_u32(&bars[2 + NST + s]); };
-  auto s_full = [&](uint32_t t) { return smem_u32(&bars[2 + 2 * NST + t]); };
-  auto p_full = [&](uint32_t t) { return smem_u32(&bars[2 + 2 * NST + NQT + t]); };
-  auto o_full = [&](uint32_t t) { return smem_u32(&bars[2 + 2 * NST + 2 * NQT + t]); };
-  auto o_empty = [&](uint32_t t) { return smem_u32(&bars[2 + 2 * NST + 3 * NQT + t]); };
-  auto v_seen = [&](uint32_t i) { return smem_u32(&bars[2 + 2 * NST + 4 * NQT + i]); };
-  auto x_full = [&](uint32_t t) { return smem_u32(&bars[4 + 2 * NST + 4 * NQT + t]); };
-  const uint32_t drain = smem_u32(&bars[6 + 2 * NST + 4 * NQT]);
-  constexpr int NBARS = 7 + 2 * NST + 4 * NQT;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const uint32_t q_full = bar(0), q_empty = bar(1);
+  auto k_full = [&](uint32_t n) { return bar(2 + n % NK); };
+  auto k_empty = [&](uint32_t n) { return bar(4 + n % NK); };
+  auto v_full = [&](uint32_t n) { return bar(6 + n % NV); };
+  auto v_empty = [&](uint32_t n) { return bar(9 + n % NV); };
+  auto s_full = [&](uint32_t n) { return bar(12 + n % NS); };
+  auto p_full = [&](uint32_t n) { return bar(15 + (n & 1)); };
+  auto pv_done = [&](uint32_t n) { return bar(17 + (n & 1)); };
+  auto v_seen = [&](uint32_t n) { return bar(19 + n % NV); };
+  auto x_full = [&](uint32_t n) { return bar(22 + (n & 1)); };
+  auto m_ready = [&](uint32_t n) { return bar(24 + (n & 1)); };
+  const uint32_t o_full = bar(26), o_empty = bar(27), e_full = bar(28), drain = bar(29);
+  constexpr int NBARS = 31;   // (drain: one for each issuing thread)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile uint32_t* const bad = tmem_slot + 2;   // [2][4]: keys of a looked-at block whose V is not finite
+  volatile uint32_t* const bad = tmem_slot + 2;   // [NV][4]: keys of a block whose V is not finite
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(kv_full(s), 1);
-      mbar_init(kv_empty(s), 3);   // the MMA thread's commit, warps 2 and 3
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(k_full(i), 1);
+      mbar_init(k_empty(i), 1);
     }
-    for (int t = 0; t < NQT; ++t) {
-      mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 256);
-      mbar_init(o_full(t), 1);
-      mbar_init(o_empty(t), 256);
-      mbar_init(x_full(t), 256);
-      mbar_init(v_seen(t), 64);
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(v_full(i), 1);
+      mbar_init(v_empty(i), 2);   // the issuing thread's commit, warp 2
+      mbar_init(v_seen(i), 32);
     }
+    for (int i = 0; i < NS; ++i) mbar_init(s_full(i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(p_full(i), 256);
+      mbar_init(pv_done(i), 1);
+      mbar_init(x_full(i), 256);
+      mbar_init(m_ready(i), 256);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 512);
+    mbar_init(e_full, 512);
     mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -240,245 +289,223 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   pdl_wait();
   pdl_launch_dependents();
+
+  Walk w;
   // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
     regs_shrink<64>();
     if (warp == 0) {
       if (lane == 0) {
-        // ------------------------------------------------------------ producer
-        uint32_t st = 0, ph = 0, nu = 0;
-        int64_t issued = 0;
-        bool ok = true;
-        int32_t r = 0;
-        for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-          const Unit x = decode_unit(P, u);
-          if (x.jmin >= x.jmax) continue;
-          if (!wait_bounded(q_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
-          mbar_arrive_expect_tx(q_full, (x.any(0) + x.any(1)) * TILE_BYTES);
-          for (int t = 0; t < NQT; ++t) {
-            if (!x.any(t)) continue;
+        // ------------------------------------------------- Q, K and V loads
+        // K runs NK blocks ahead of V: a walk each.
+        Walk a;
+        int64_t nk = 0;
+        uint32_t nv = 0, units = 0;
+        auto load_k = [&]() {
+          if (a.done) return true;
+          if (a.first) {
+            if (!wait_bounded(q_empty, (a.nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) return false;
+            mbar_arrive_expect_tx(q_full, TILE_BYTES);
             for (int c = 0; c < 2; ++c)
-              tma_load_3d(sQ(t) + c * HALF_BYTES, &mapQ, q_full, x.head * DH + c * 64,
-                          (x.qb0 + t) * BQ, x.shard);
+              tma_load_3d(sQ + c * HALF_BYTES, &mapQ, q_full, a.x.head * DH + c * 64, a.x.qb * BQ,
+                          a.x.shard);
+            ++units;
           }
-          ++nu;
-          for (int32_t j = x.jmin; j < x.jmax; ++j) {
-            if (!wait_bounded(kv_empty(st), ph ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
-              ok = false;
-              break;
-            }
-            if (issued != P.debug_drop) {
-              mbar_arrive_expect_tx(kv_full(st), 2 * TILE_BYTES);
-              for (int c = 0; c < 2; ++c) {
-                tma_load_3d(sK(st) + c * HALF_BYTES, &mapK, kv_full(st), x.kvh * DH + c * 64, j * BKV,
-                            x.shard);
-                tma_load_3d(sV(st) + c * HALF_BYTES, &mapV, kv_full(st), x.kvh * DH + c * 64, j * BKV,
-                            x.shard);
-              }
-            }
-            ++issued;
-            if (++st == NST) {
-              st = 0;
-              ph ^= 1u;
-            }
+          if (!wait_bounded(k_empty(a.n), ((a.n / NK) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty))
+            return false;
+          if (nk != P.debug_drop) {
+            mbar_arrive_expect_tx(k_full(a.n), TILE_BYTES);
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d(sK(a.n) + c * HALF_BYTES, &mapK, k_full(a.n), a.x.kvh * DH + c * 64,
+                          a.j * BKV, a.x.shard);
           }
+          ++nk;
+          a.next(P);
+          return true;
+        };
+        a.begin(P);
+        bool ok = true;
+        for (int i = 0; ok && i < NK; ++i) ok = load_k();
+        for (w.begin(P); ok && !w.done; w.next(P)) {
+          if (!wait_bounded(v_empty(w.n), ((w.n / NV) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) break;
+          mbar_arrive_expect_tx(v_full(w.n), TILE_BYTES);
+          for (int c = 0; c < 2; ++c)
+            tma_load_3d(sV(w.n) + c * HALF_BYTES, &mapV, v_full(w.n), w.x.kvh * DH + c * 64, w.j * BKV,
+                        w.x.shard);
+          ++nv;
+          ok = load_k();
         }
         // Teardown: let the last loads land before shared memory is released.
-        if (nu > 0) wait_teardown(q_full, (nu - 1) & 1, P.wait);
-        const int64_t first = issued > NST ? issued - NST : 0;
-        for (int64_t q = first; q < issued; ++q) {
-          if (q == P.debug_drop) continue;
-          wait_teardown(kv_full(static_cast<uint32_t>(q % NST)), static_cast<uint32_t>((q / NST) & 1),
-                        P.wait);
-        }
+        if (units > 0) wait_teardown(q_full, (units - 1) & 1, P.wait);
+        for (int64_t i = nk > NK ? nk - NK : 0; i < nk; ++i)
+          if (i != P.debug_drop)
+            wait_teardown(k_full(static_cast<uint32_t>(i)), static_cast<uint32_t>((i / NK) & 1), P.wait);
+        for (uint32_t i = nv > NV ? nv - NV : 0; i < nv; ++i) wait_teardown(v_full(i), (i / NV) & 1, P.wait);
       }
       __syncwarp();
     } else if (warp == 1) {
       if (lane == 0) {
-        // ---------------------------------------------------------- MMA issuer
-        uint32_t kv_n = 0, nu = 0;     // K/V blocks and units so far
-        uint32_t pv[NQT] = {0, 0};     // O += P V products per tile
-        uint32_t ou[NQT] = {0, 0};     // units per tile with an output
-        bool ok = true;
-        auto wait_kv = [&](uint32_t n) {
-          return wait_bounded(kv_full(n % NST), (n / NST) & 1, abort_flag, P.wait, kErrWaitFull);
-        };
-        auto issue_s = [&](uint32_t t, uint32_t n) {
-          const uint32_t kst = n % NST;
-  #pragma unroll
+        // --------------------------------------------------- S = Q K^T issuer
+        for (w.begin(P); !w.done; w.next(P)) {
+          if ((w.first && !wait_bounded(q_full, w.nu & 1, abort_flag, P.wait, kErrWaitFull)) ||
+              !wait_bounded(k_full(w.n), (w.n / NK) & 1, abort_flag, P.wait, kErrWaitFull) ||
+              // the buffer's last probabilities have been used
+              (w.n >= NS && !wait_bounded(pv_done(w.n - NS), ((w.n - NS) >> 1) & 1, abort_flag, P.wait,
+                                          kErrWaitAttn)))
+            break;
+          tc_fence_after();
+          const uint32_t k = sK(w.n), d = tmem_base + (w.n % NS) * BKV;
+#pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) {
             const uint32_t off = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-            tc_mma_f16(tmem_base + t * BKV, smem_desc_sw128(sQ(t) + off, 16, 1024),
-                       smem_desc_sw128(sK(kst) + off, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
+            tc_mma_f16(d, smem_desc_sw128(sQ + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024),
+                       IDESC_S, kk > 0 ? 1u : 0u);
           }
-          tc_commit(s_full(t));
-        };
-        int32_t r = 0;
-        for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-          const Unit x = decode_unit(P, u);
-          if (x.jmin >= x.jmax) continue;
-          if (!wait_bounded(q_full, nu & 1, abort_flag, P.wait, kErrWaitAttn)) break;
-          ++nu;
-          // Only the Q K^T products read Q: it is handed back once the last one
-          // of every tile is issued.
-          int s_left = x.any(0) + x.any(1);
-          auto start_s = [&](int t, int32_t j) {
-            issue_s(t, kv_n + (j - x.jmin));
-            if (j + 1 == x.t[t].je && --s_left == 0) tc_commit(q_empty);
-          };
-          if (!wait_kv(kv_n)) break;
-          tc_fence_after();
-  #pragma unroll
-          for (int t = 0; t < NQT; ++t)
-            if (x.active(t, x.jmin)) start_s(t, x.jmin);
-          for (int32_t j = x.jmin; ok && j < x.jmax; ++j) {
-            const uint32_t n = kv_n + (j - x.jmin), vst = n % NST;
-            const bool a0 = x.active(0, j), a1 = x.active(1, j);
-            if (!a0 && !a1) {   // no tile reads this block
-              if (!wait_kv(n)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive(kv_empty(vst));
-            }
-  #pragma unroll
-            for (int t = 0; t < NQT; ++t) {
-              const bool act = t == 0 ? a0 : a1;
-              if (act) {
-                if (j == x.t[t].jb && ou[t] > 0 &&
-                    !wait_bounded(o_empty(t), (ou[t] - 1) & 1, abort_flag, P.wait, kErrWaitAttn)) {
-                  ok = false;
-                  break;
-                }
-                if (!wait_bounded(p_full(t), pv[t] & 1, abort_flag, P.wait, kErrWaitAttn)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-  #pragma unroll
-                for (int kk = 0; kk < BKV / 16; ++kk) {
-                  const uint64_t bdesc = smem_desc_sw128(sV(vst) + kk * 16 * 128, HALF_BYTES, 1024);
-                  tc_mma_f16_ts(tmem_base + O_COL0 + t * DH,
-                                tmem_base + t * BKV + (kk >> 2) * 64 + (kk & 3) * 8, bdesc, IDESC_O,
-                                (j > x.t[t].jb || kk > 0) ? 1u : 0u);
-                }
-                ++pv[t];
-                if (t == NQT - 1 || !a1) tc_commit(kv_empty(vst));   // the block's last reader
-              }
-              if (x.active(t, j + 1)) {
-                if (!wait_kv(n + 1)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                start_s(t, j + 1);
-              } else if (act) {
-                tc_commit(o_full(t));
-              }
-            }
-          }
-          if (!ok) break;
-  #pragma unroll
-          for (int t = 0; t < NQT; ++t)
-            if (x.any(t)) ++ou[t];
-          kv_n += x.jmax - x.jmin;
+          tc_commit(s_full(w.n));
+          tc_commit(k_empty(w.n));
+          if (w.last()) tc_commit(q_empty);
         }
         tc_commit(drain);
         wait_teardown(drain, 0, P.wait);
       }
       __syncwarp();
-    } else {
-      // ------------------------------------- values in blocks that a mask cuts
-      uint32_t n = 0, looked = 0;
-      bool ok = true;
-      int32_t r = 0;
-      for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-        const Unit x = decode_unit(P, u);
-        for (int32_t j = x.jmin; j < x.jmax; ++j, ++n) {
-          const uint32_t st = n % NST;
-          ok = wait_bounded(kv_full(st), (n / NST) & 1, abort_flag, P.wait, kErrWaitFull);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (x.cut(j)) {
-  #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = h * 64 + (warp - 2) * 32 + lane;
-              const bool is_bad = row_not_finite(sV(st), row);
-              const uint32_t w = __ballot_sync(0xffffffffu, is_bad);
-              if (is_bad) zero_row(sV(st), row);
-              if (lane == 0) bad[(looked & 1) * 4 + h * 2 + (warp - 2)] = w;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(v_seen(looked & 1));
-            ++looked;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kv_empty(st));
+    } else if (warp == 3) {
+      if (lane == 0) {
+        // ------------------------------------------------- O += P V issuer
+        for (w.begin(P); !w.done; w.next(P)) {
+          if ((w.first && w.nu > 0 &&
+               !wait_bounded(o_empty, (w.nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn)) ||
+              !wait_bounded(v_seen(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull) ||
+              !wait_bounded(p_full(w.n), (w.n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn))
+            break;
+          tc_fence_after();
+          const uint32_t v = sV(w.n), pa = tmem_base + (w.n % NS) * BKV;
+#pragma unroll
+          for (int kk = 0; kk < BKV / 16; ++kk)
+            tc_mma_f16_ts(tmem_base + O_COL0, pa + (kk >> 2) * 64 + (kk & 3) * 8,
+                          smem_desc_sw128(v + kk * 16 * 128, HALF_BYTES, 1024), IDESC_O,
+                          (!w.first || kk > 0) ? 1u : 0u);
+          tc_commit(pv_done(w.n));
+          tc_commit(v_empty(w.n));
+          if (w.last()) tc_commit(o_full);
         }
+        tc_commit(drain + 8);
+        wait_teardown(drain + 8, 0, P.wait);
+      }
+      __syncwarp();
+    } else {
+      // ----------------------------------- values in blocks that a mask cuts
+      for (w.begin(P); !w.done; w.next(P)) {
+        bool ok = wait_bounded(v_full(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (!w.x.t.whole(w.j)) {
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            const int row = h * 32 + lane;
+            const bool is_bad = row_not_finite(sV(w.n), row);
+            const uint32_t m = __ballot_sync(0xffffffffu, is_bad);
+            if (is_bad) zero_row(sV(w.n), row);
+            if (lane == 0) bad[(w.n % NV) * 4 + h] = m;
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(v_seen(w.n));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_empty(w.n));
       }
     }
   } else {
     regs_grow<104>();
     // ------------------------------------------------------- softmax / output
-    // thread = row and column half: scores [64 half, 64 half + 64) of a block,
-    // and those columns of O
-    const int t = (warp - 4) / 8;
+    // thread = row and column half: scores [64 half, 64 half + 64) of its
+    // group's blocks, and 32 columns of O
+    const int g = (warp - 4) / 8;
     const int half = ((warp - 4) / 4) & 1;
+    const int part = g * 2 + half;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem_base + lane_off + t * BKV + half * 64;
-    const uint32_t tO = tmem_base + lane_off + O_COL0 + t * DH + half * 64;
+    const uint32_t tO = tmem_base + lane_off + O_COL0;
     constexpr bool HAS_MAX = MODE != kCap;
     const ScoreConsts& S = P.s;
-    uint32_t sc = 0, uc = 0, looked = 0, xc = 0;
     bool ok = true;
-    // hands v to the row's other half and takes its
-    auto swap_halves = [&](float v, float* other) {
-      xch[((t * 2 + (xc & 1)) * 2 + half) * BQ + row] = v;
-      mbar_arrive(x_full(t));
-      const bool got = wait_bounded(x_full(t), xc & 1, abort_flag, P.wait, kErrWaitAttn);
-      *other = xch[((t * 2 + (xc & 1)) * 2 + (half ^ 1)) * BQ + row];
-      ++xc;
+    float m = HAS_MAX ? -INFINITY : 0.0f, l = 0.0f;
+    bool poison = false, lost = false;
+    int2 seen = make_int2(0, -1);
+    float slope2 = 0.0f;
+    // the unit whose end is still to be done
+    bool pending = false;
+    uint32_t p_nu = 0;
+    int64_t p_row = -1;       // its row in O [.. * head_dim], -1: not stored
+    int64_t p_lse = 0;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      const bool got = wait_bounded(b, parity, abort_flag, P.wait, kErrWaitAttn);
       return __all_sync(0xffffffffu, got) != 0;
     };
-    int32_t r = 0;
-    for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-      const Unit x = decode_unit(P, u);
-      const TileSpan mine = x.span(t);
-      const int32_t q0 = (x.qb0 + t) * BQ;
-      const int32_t q = q0 + row;
-      const int2 seen = row_span(P.mask, q, P.T, P.causal);
-      float slope2 = 0.0f;
-      if (MODE == kBias || MODE == kCapAny)
-        slope2 = P.slopes != nullptr ? 1.4426950408889634f * P.slopes[x.shard * P.hq + x.head] : 0.0f;
-      float m = HAS_MAX ? -INFINITY : 0.0f, l = 0.0f;
-      bool poison = false, lost = false;
-      for (int32_t j = x.jmin; j < x.jmax; ++j) {
-        const bool cut = x.cut(j);
-        if (!x.active(t, j)) {
-          looked += cut;
-          continue;
+    auto finish = [&]() {
+      pending = false;
+      if (!wait(e_full, p_nu & 1) || !wait(o_full, p_nu & 1)) return false;
+      tc_fence_after();
+      const volatile float* e = ends + (p_nu & 1) * 3 * 4 * BQ + row;
+      // the row's sum over its four threads, each under its own last maximum
+      float M = 0.0f;
+      if (HAS_MAX) {
+        M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) M = max3_nan(M, e[(4 + i) * BQ], M);
+      }
+      float L = 0.0f, mark = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float mi = HAS_MAX ? e[(4 + i) * BQ] : 0.0f, li = e[i * BQ];
+        L += mi == M ? li : li * ex2(mi - M);
+        mark += e[(8 + i) * BQ];
+      }
+      const float inv_l = mark != 0.0f ? NAN : L == 0.0f ? 0.0f : 1.0f / L;
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tO + part * 32, v);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(o_empty);
+      if (p_row >= 0) {
+        __nv_bfloat16* dst = P.O + p_row + part * 32;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = pack2(__uint_as_float(v[q * 8 + 2 * i]) * inv_l,
+                         __uint_as_float(v[q * 8 + 2 * i + 1]) * inv_l);
+          *reinterpret_cast<uint4*>(dst + q * 8) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        ok = wait_bounded(s_full(t), sc & 1, abort_flag, P.wait, kErrWaitAttn);
-        const int32_t key0 = j * BKV + half * 64, rl = seen.x - key0, rh = seen.y - key0;
-        if (ok && cut) {
-          ok = wait_bounded(v_seen(looked & 1), (looked >> 1) & 1, abort_flag, P.wait, kErrWaitAttn);
-          if (ok) {
-            const volatile uint32_t* b = bad + (looked & 1) * 4 + half * 2;
-            if (b[0] | b[1]) {
-              for (int e = 0; e < 64; ++e)
-                poison |= e >= rl && e < rh && ((b[e >> 5] >> (e & 31)) & 1);
-            }
-          }
-          ++looked;
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        if (part == 0 && P.LSE != nullptr)
+          P.LSE[p_lse] = L == 0.0f ? -INFINITY : 0.6931471805599453f * M + logf(L);
+      }
+      return true;
+    };
+    for (w.begin(P); !w.done; w.next(P)) {
+      const uint32_t n = w.n;
+      const int32_t q = w.x.qb * BQ + row;
+      if (w.first) {
+        seen = row_span(P.mask, q, P.T, P.causal);
+        if (MODE == kBias || MODE == kCapAny)
+          slope2 = P.slopes != nullptr
+                       ? 1.4426950408889634f * P.slopes[w.x.shard * P.hq + w.x.head]
+                       : 0.0f;
+      }
+      if (static_cast<int>(n & 1) == g) {
+        // (behind the unit's first block the previous unit's end must be done:
+        // the values' products wait for it, and a rescaled O for them)
+        if (pending && !w.first && !finish()) break;
+        const uint32_t tS = tmem_base + lane_off + (n % NS) * BKV + half * 64;
+        const int32_t key0 = w.j * BKV + half * 64, rl = seen.x - key0, rh = seen.y - key0;
+        const bool whole = w.x.t.whole(w.j);
+        ok = wait(s_full(n), (n / NS) & 1);
         if (!ok) break;
         tc_fence_after();
-        const bool whole = mine.whole(j);
         const float dist0 = static_cast<float>(key0 - q);
-        const int side = j * BKV + BKV - 1 <= q0 ? -1 : j * BKV >= q0 + BQ - 1 ? 1 : 0;
+        const int side = w.j * BKV + BKV - 1 <= w.x.qb * BQ ? -1 : w.j * BKV >= w.x.qb * BQ + BQ - 1 ? 1 : 0;
         uint64_t sum2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
         // (loops kept rolled: the instruction cache holds one chunk's code)
         if (HAS_MAX) {
@@ -498,26 +525,45 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (MODE != kPlain) tmem_st_32x32b_x32(tS + c * 32, v);
           }
           if (MODE != kPlain) tmem_st_wait();
-          float m_cand = max3_nan(acc[0], acc[1], acc[1]), other;
-          ok = swap_halves(m_cand, &other);
-          if (!ok) break;
+          float m_cand = max3_nan(acc[0], acc[1], acc[1]);
+          // the other group's maximum first: its arrival also says that this
+          // group's last exchange has been read
+          if (n > 0 && !wait(m_ready(n - 1), ((n - 1) >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const float m_prev = w.first ? -INFINITY : run_m[(g ^ 1) * BQ + row];
+          xch[part * BQ + row] = m_cand;
+          mbar_arrive(x_full(n));
+          if (!wait(x_full(n), (n >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const float other = xch[(part ^ 1) * BQ + row];
           m_cand = max3_nan(m_cand, other, other);
           if (MODE == kPlain) m_cand *= S.scale_log2;
-          const bool grow = !(m_cand <= m + RESCALE_LOG2);   // NaN too: it then stays in the sum
-          const float alpha = grow ? ex2(m - m_cand) : 1.0f;
-          if (grow) m = m_cand;
-          l *= alpha;
-          if (j > mine.jb && __any_sync(0xffffffffu, grow)) {
-            // O += P V of the previous block has completed: it was issued
-            // before this score block, whose commit we waited for
+          const bool grow = !(m_cand <= m_prev + RESCALE_LOG2);   // NaN too: it then stays
+          const float m_new = grow ? m_cand : m_prev;
+          if (half == 0) run_m[g * BQ + row] = m_new;
+          mbar_arrive(m_ready(n));
+          if (m != m_new) l *= ex2(m - m_new);
+          m = m_new;
+          if (!w.first && __any_sync(0xffffffffu, grow)) {
+            // O is whole once P V of the block before this one is done
+            if (!wait(pv_done(n - 1), ((n - 1) >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float alpha = grow ? ex2(m_prev - m_new) : 1.0f;
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
               uint32_t v[32];
-              tmem_ld_32x32b_x32(tO + c * 32, v);
+              tmem_ld_32x32b_x32(tO + half * 64 + c * 32, v);
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st_32x32b_x32(tO + c * 32, v);
+              tmem_st_32x32b_x32(tO + half * 64 + c * 32, v);
             }
           }
         }
@@ -535,57 +581,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_st_32x32b_x16(tS + c * 16, pk);
         }
         tmem_st_wait();
+        if (!whole) {   // keys in sight whose value is not finite
+          if (!wait(v_seen(n), (n / NV) & 1)) {
+            ok = false;
+            break;
+          }
+          const volatile uint32_t* b = bad + (n % NV) * 4 + half * 2;
+          if (b[0] | b[1]) {
+            for (int e = 0; e < 64; ++e)
+              poison |= e >= rl && e < rh && ((b[e >> 5] >> (e & 31)) & 1);
+          }
+        }
         tc_fence_before();
-        mbar_arrive(p_full(t));
+        mbar_arrive(p_full(n));
         float s0, s1, s2, s3;
         f2_unpack(sum2[0], s0, s1);
         f2_unpack(sum2[1], s2, s3);
         l += (s0 + s1) + (s2 + s3);
-        ++sc;
-      }
-      if (!ok) break;
-      if (!x.any(t)) continue;
-      // the row's sum over both halves; NaN where a half lost a NaN score, and
-      // a mark where one saw a key whose value is not finite
-      float other;
-      ok = swap_halves(lost ? NAN : l, &other);
-      if (!ok) break;
-      l = lost ? NAN : half == 0 ? l + other : other + l;
-      ok = swap_halves(poison ? 1.0f : 0.0f, &other);
-      if (!ok) break;
-      poison |= other != 0.0f;
-      ok = wait_bounded(o_full(t), uc & 1, abort_flag, P.wait, kErrWaitAttn);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const float inv_l = poison ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
-      const bool store = q < P.T && seen.y >= 0;   // rows of no document stay as they were
-      __nv_bfloat16* dst =
-          P.O + ((static_cast<int64_t>(x.shard) * P.T + q) * P.hq + x.head) * DH + half * 64;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(tO + c * 32, v);
-        tmem_ld_wait();
-        if (store) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[i] = pack2(__uint_as_float(v[g * 8 + 2 * i]) * inv_l,
-                           __uint_as_float(v[g * 8 + 2 * i + 1]) * inv_l);
-            *reinterpret_cast<uint4*>(dst + c * 32 + g * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+        if (pending && !finish()) {
+          ok = false;
+          break;
         }
       }
-      if (store && half == 0 && P.LSE != nullptr)
-        P.LSE[(static_cast<int64_t>(x.shard) * P.hq + x.head) * P.T + q] =
-            l == 0.0f ? -INFINITY : 0.6931471805599453f * m + logf(l);
-      tc_fence_before();
-      mbar_arrive(o_empty(t));
-      ++uc;
+      if (w.last()) {
+        if (pending && !finish()) {
+          ok = false;
+          break;
+        }
+        // this unit's sums; its end follows
+        volatile float* e = ends + (w.nu & 1) * 3 * 4 * BQ + row;
+        e[part * BQ] = lost ? NAN : l;
+        if (HAS_MAX) e[(4 + part) * BQ] = m;
+        e[(8 + part) * BQ] = poison ? 1.0f : 0.0f;
+        mbar_arrive(e_full);
+        pending = true;
+        p_nu = w.nu;
+        const bool store = q < P.T && seen.y >= 0;   // rows of no document stay as they were
+        p_row = store ? ((static_cast<int64_t>(w.x.shard) * P.T + q) * P.hq + w.x.head) * DH : -1;
+        p_lse = (static_cast<int64_t>(w.x.shard) * P.hq + w.x.head) * P.T + q;
+        m = HAS_MAX ? -INFINITY : 0.0f;
+        l = 0.0f;
+        poison = lost = false;
+      }
     }
+    if (ok && pending) finish();
   }
 
   __syncthreads();
@@ -737,8 +776,7 @@ tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a) {
   prm.hkv = a.hkv;
   prm.group = a.hq / a.hkv;
   prm.q_blocks = ceil_div(a.T, BQ);
-  prm.q_pairs = ceil_div(prm.q_blocks, NQT);
-  prm.num_units = a.p * a.hq * prm.q_pairs;
+  prm.num_units = a.p * a.hq * prm.q_blocks;
   prm.causal = a.causal ? 1 : 0;
   prm.mask = mask_plan(a.mask, a.T);
   prm.s = score_consts(a.scale, a.cap);

@@ -60,6 +60,17 @@ def test_matches_oracle(case):
     _check(case, *_run(case), heads=heads)
 
 
+@pytest.mark.parametrize("case", [
+    dict(p=2, T=700, h=96, hkv=48, off=[0, 1, 128, 129, 384, 650], slopes=1.0),
+    dict(p=1, T=600, h=64, hkv=64, off=list(range(0, 601, 25)), cap=30.0),
+    dict(p=2, T=500, h=128, hkv=64, cap=50.0), dict(p=1, T=130, h=200, hkv=200),
+    dict(p=1, T=300, h=120, hkv=8, off=[0, 0, 3, 260], std=3.0)], ids=["docs", "short", "causal", "tiny", "peaked"])
+def test_several_units_a_block_of_threads(case):
+    """More (head, tile) units than the GPU has SMs, masks in most blocks."""
+    last = (case["p"] - 1, case["h"] // case["p"] - 1)
+    _check(case, *_run(case), heads={(0, 0), (0, 17), last})
+
+
 def test_no_options_is_plain_attention():
     p, T, h = 2, 200, 4
     rng = np.random.default_rng(0)
