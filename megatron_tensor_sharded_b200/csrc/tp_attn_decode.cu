@@ -69,7 +69,7 @@ struct DecodeParams {
 // Keys in sight of sequence b's token, the appended one included; -1: the
 // slot is unused, -2: the length does not fit the cache.
 __device__ __forceinline__ int32_t keys_of(const DecodeParams& P, int32_t b) {
-  const int32_t n = P.len[b];
+  const int32_t n = __ldcg(P.len + b);   // (from L2: the join reads it before it waits)
   if (n < 0) return -1;
   const int64_t keys = static_cast<int64_t>(n) + (P.Kn != nullptr ? 1 : 0);
   return keys > P.capacity ? -2 : static_cast<int32_t>(keys);

@@ -373,8 +373,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const uint32_t tS = tm, tdP = tm + 128, tdV = tm + 256, tdK = tm + 384;
-  // The dq kernel behind this one reads only what was complete before this
-  // point; it may start on SMs that this one leaves (it waits at its end).
   pdl_wait();
   pdl_launch_dependents();
 
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
           const KeyUnit x = key_unit(P, u);
           if (x.ia >= x.ib) continue;
-          if (!wait_bounded(kv_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
+          if (!wait_asleep(kv_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
           mbar_arrive_expect_tx(kv_full, 2 * TILE_BYTES);
           load_tile(sK, &mapK, kv_full, x.kvh, x.kb * BT, x.shard);
           load_tile(sV, &mapV, kv_full, x.kvh, x.kb * BT, x.shard);
@@ -398,13 +396,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int32_t g = 0; ok && g < P.group; ++g) {
             const int32_t head = x.kvh * P.group + g;
             for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
-              if (!wait_bounded(q_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+              if (!wait_asleep(q_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
                 ok = false;
                 break;
               }
               mbar_arrive_expect_tx(q_full(n), TILE_BYTES);
               load_tile(sQ(n), &mapQ, q_full(n), head, i * BT, x.shard);
-              if (!wait_bounded(do_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+              if (!wait_asleep(do_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
                 ok = false;
                 ++nq;
                 break;
@@ -430,17 +428,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t n = 0, nu = 0;
         bool ok = true;
         auto wait_q = [&](uint32_t m) {
-          return wait_bounded(q_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull);
+          return wait_asleep(q_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull);
         };
         auto wait_do = [&](uint32_t m) {
-          return wait_bounded(do_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull);
+          return wait_asleep(do_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull);
         };
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
           const KeyUnit x = key_unit(P, u);
           const int32_t steps = P.group * (x.ib - x.ia);
           if (x.ia >= x.ib) continue;
-          if (!wait_bounded(kv_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_q(n)) break;
+          if (!wait_asleep(kv_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_q(n)) break;
           tc_fence_after();
           mma_tiles(tS, sK, sQ(n));
           tc_commit(s_full);
@@ -453,7 +451,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const bool more = s + 1 < steps;
             if (more) {
               // the next scores as soon as the warps hold this step's
-              if (!wait_bounded(s_free, n & 1, abort_flag, P.wait, kErrWaitAttn) || !wait_q(n + 1)) {
+              if (!wait_asleep(s_free, n & 1, abort_flag, P.wait, kErrWaitAttn) || !wait_q(n + 1)) {
                 ok = false;
                 break;
               }
@@ -461,9 +459,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               mma_tiles(tS, sK, sQ(n + 1));
               tc_commit(s_full);
             }
-            if (!wait_bounded(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
+            if (!wait_asleep(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
                 (s == 0 && nu > 0 &&
-                 !wait_bounded(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
+                 !wait_asleep(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
               ok = false;
               break;
             }
@@ -512,7 +510,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               lse[h] = in ? -kLog2e * P.LSE[row0 + q] : -INFINITY;   // P = 0 behind the last row
               dl[h] = in ? -P.delta[row0 + q] : 0.0f;
             }
-            ok = wait_bounded(do_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty);
+            ok = wait_asleep(do_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
 #pragma unroll
@@ -521,8 +519,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               sts(vec(n, 1) + (h * 64 + me) * 4, dl[h]);
             }
             if (me == 0) cut_flag[n % NB] = cut;
-            ok = wait_bounded(q_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull) &&
-                 (!cut || wait_bounded(do_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitFull));
+            ok = wait_asleep(q_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull) &&
+                 (!cut || wait_asleep(do_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitFull));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (cut) {
@@ -565,8 +563,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float slope2 = 0.0f;
         if (BIAS) slope2 = kLog2e * P.slopes[x.shard * P.hq + x.kvh * P.group + g];
         for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
-          ok = wait_bounded(vec_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitAttn) &&
-               wait_bounded(s_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
+          ok = wait_asleep(vec_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitAttn) &&
+               wait_asleep(s_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -590,7 +588,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive(s_free);
           prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut,
                                 [&](int e) { return lds2(vl + e * 4); }, sees);
-          ok = wait_bounded(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
+          ok = wait_asleep(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -606,7 +604,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      ok = wait_bounded(acc_full, nu & 1, abort_flag, P.wait, kErrWaitAttn);
+      ok = wait_asleep(acc_full, nu & 1, abort_flag, P.wait, kErrWaitAttn);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -673,12 +671,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto v_empty = [&](uint32_t n) { return smem_u32(&bars[10 + n % NB]); };
   auto s_full = [&](uint32_t b) { return smem_u32(&bars[12 + b]); };
   const uint32_t dp_full = smem_u32(&bars[14]), dp_free = smem_u32(&bars[15]);
-  const uint32_t ds_full = smem_u32(&bars[16]);
-  const uint32_t acc_full = smem_u32(&bars[17]), acc_empty = smem_u32(&bars[18]);
+  // (two: the warps may finish step n + 1 before the MMA thread has seen step n)
+  auto ds_full = [&](uint32_t n) { return smem_u32(&bars[16 + (n & 1)]); };
+  const uint32_t acc_full = smem_u32(&bars[18]), acc_empty = smem_u32(&bars[19]);
   // one a ring slot: warps 2 and 3 may be that many blocks ahead
-  auto k_seen = [&](uint32_t i) { return smem_u32(&bars[19 + i % NA]); };
-  const uint32_t drain = smem_u32(&bars[19 + NA]);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (20 + NA));
+  auto k_seen = [&](uint32_t i) { return smem_u32(&bars[20 + i % NA]); };
+  const uint32_t drain = smem_u32(&bars[20 + NA]);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (21 + NA));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -697,7 +696,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int s = 0; s < 2; ++s) mbar_init(s_full(s), 1);
     mbar_init(dp_full, 1);
     mbar_init(dp_free, ARITH);
-    mbar_init(ds_full, ARITH);
+    mbar_init(ds_full(0), ARITH);
+    mbar_init(ds_full(1), ARITH);
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, ARITH);
     mbar_init(drain, 1);
@@ -720,6 +720,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const uint32_t tdP = tm + 256, tdQ = tm + 384;   // S buffers at 0 and 128
+  pdl_wait();
+  pdl_launch_dependents();
 
   // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
@@ -733,20 +735,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
           const QueryUnit x = query_unit(P, u);
           if (x.t.jb >= x.t.je) continue;
-          if (!wait_bounded(qd_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
+          if (!wait_asleep(qd_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
           mbar_arrive_expect_tx(qd_full, 2 * TILE_BYTES);
           load_tile(sQ, &mapQ, qd_full, x.head, x.qb * BT, x.shard);
           load_tile(sdO, &mapdO, qd_full, x.head, x.qb * BT, x.shard);
           ++nu;
           for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
-            if (!wait_bounded(k_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+            if (!wait_asleep(k_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
               ok = false;
               break;
             }
             mbar_arrive_expect_tx(k_full(n), TILE_BYTES);
             load_tile(sK(n), &mapK, k_full(n), x.kvh, j * BT, x.shard);
             ++nk;
-            if (!wait_bounded(v_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
+            if (!wait_asleep(v_empty(n), ((n / NB) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
               ok = false;
               break;
             }
@@ -768,14 +770,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t n = 0, nu = 0;
         bool ok = true;
         auto issue_s = [&](uint32_t m) {
-          if (!wait_bounded(k_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
+          if (!wait_asleep(k_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
           tc_fence_after();
           mma_tiles(tm + (m & 1) * 128, sQ, sK(m));
           tc_commit(s_full(m & 1));
           return true;
         };
         auto issue_dp = [&](uint32_t m) {
-          if (!wait_bounded(v_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
+          if (!wait_asleep(v_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
           tc_fence_after();
           mma_tiles(tdP, sdO, sV(m));
           tc_commit(v_empty(m));
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const QueryUnit x = query_unit(P, u);
           const int32_t steps = x.t.je - x.t.jb;
           if (steps <= 0) continue;
-          if (!wait_bounded(qd_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !issue_s(n) ||
+          if (!wait_asleep(qd_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !issue_s(n) ||
               !issue_dp(n))
             break;
           if (steps == 1)
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int32_t s = 0; s < steps; ++s, ++n) {
             if (s + 1 < steps) {
               // the warps have read dP of this step
-              ok = wait_bounded(dp_free, n & 1, abort_flag, P.wait, kErrWaitAttn);
+              ok = wait_asleep(dp_free, n & 1, abort_flag, P.wait, kErrWaitAttn);
               if (ok) {
                 tc_fence_after();
                 ok = issue_dp(n + 1);
@@ -805,9 +807,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (!ok) break;
               if (s + 2 == steps) tc_commit(qd_empty);
             }
-            if (!wait_bounded(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
+            if (!wait_asleep(ds_full(n), (n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn) ||
                 (s == 0 && nu > 0 &&
-                 !wait_bounded(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
+                 !wait_asleep(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
               ok = false;
               break;
             }
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
         const QueryUnit x = query_unit(P, u);
         for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
-          ok = wait_bounded(k_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull);
+          ok = wait_asleep(k_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (!x.t.whole(j)) {
@@ -877,9 +879,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
         const uint32_t b = n & 1, tS = tm + b * 128 + off;
         const bool cut = !x.t.whole(j);
-        ok = wait_bounded(s_full(b), (n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn);
+        ok = wait_asleep(s_full(b), (n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn);
         if (cut) {
-          ok = ok && wait_bounded(k_seen(looked), (looked / NA) & 1, abort_flag, P.wait, kErrWaitAttn);
+          ok = ok && wait_asleep(k_seen(looked), (looked / NA) & 1, abort_flag, P.wait, kErrWaitAttn);
           ++looked;
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -895,7 +897,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_ld_wait();
         // (P itself is not stored: dQ needs dS alone)
         prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut, [&](int) { return nlse; }, sees);
-        ok = wait_bounded(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
+        ok = wait_asleep(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -907,10 +909,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_st_32x32b_x16(tS, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        mbar_arrive(ds_full(n));
       }
       if (!ok) break;
-      ok = wait_bounded(acc_full, nu & 1, abort_flag, P.wait, kErrWaitAttn);
+      ok = wait_asleep(acc_full, nu & 1, abort_flag, P.wait, kErrWaitAttn);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -927,9 +929,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tm, 512);
   }
-  // this grid must not be complete before the one it ran beside
-  pdl_wait();
-  pdl_launch_dependents();
 }
 
 template <bool CAP, bool BIAS>

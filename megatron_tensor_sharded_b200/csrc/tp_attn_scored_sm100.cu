@@ -234,13 +234,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto v_full = [&](uint32_t n) { return bar(6 + n % NV); };
   auto v_empty = [&](uint32_t n) { return bar(9 + n % NV); };
   auto s_full = [&](uint32_t n) { return bar(12 + n % NS); };
-  auto p_full = [&](uint32_t n) { return bar(15 + (n & 1)); };
-  auto pv_done = [&](uint32_t n) { return bar(17 + (n & 1)); };
-  auto v_seen = [&](uint32_t n) { return bar(19 + n % NV); };
-  auto x_full = [&](uint32_t n) { return bar(22 + (n & 1)); };
-  auto m_ready = [&](uint32_t n) { return bar(24 + (n & 1)); };
-  const uint32_t o_full = bar(26), o_empty = bar(27), e_full = bar(28), drain = bar(29);
-  constexpr int NBARS = 31;   // (drain: one for each issuing thread)
+  // Barriers of a block are as many as it can be ahead of the block whose phase
+  // somebody may still be waiting for: one a score buffer for p_full (a group
+  // may finish block n + 2 while a load holds P V of block n up) and for
+  // pv_done (a load may hold Q K^T up while P V of all its buffers completes).
+  auto p_full = [&](uint32_t n) { return bar(15 + n % NS); };
+  auto pv_done = [&](uint32_t n) { return bar(18 + n % NS); };
+  auto v_seen = [&](uint32_t n) { return bar(21 + n % NV); };
+  auto x_full = [&](uint32_t n) { return bar(24 + (n & 1)); };
+  auto m_ready = [&](uint32_t n) { return bar(26 + (n & 1)); };
+  const uint32_t o_full = bar(28), o_empty = bar(29), e_full = bar(30), drain = bar(31);
+  constexpr int NBARS = 33;   // (drain: one for each issuing thread)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * NBARS);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* const bad = tmem_slot + 2;   // [NV][4]: keys of a block whose V is not finite
@@ -258,10 +262,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(v_empty(i), 2);   // the issuing thread's commit, warp 2
       mbar_init(v_seen(i), 32);
     }
-    for (int i = 0; i < NS; ++i) mbar_init(s_full(i), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 256);
       mbar_init(pv_done(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(x_full(i), 256);
       mbar_init(m_ready(i), 256);
     }
@@ -299,19 +305,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------- Q, K and V loads
         // K runs NK blocks ahead of V: a walk each.
         Walk a;
+        a.begin(P);
         int64_t nk = 0;
         uint32_t nv = 0, units = 0;
         auto load_k = [&]() {
           if (a.done) return true;
           if (a.first) {
-            if (!wait_bounded(q_empty, (a.nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) return false;
+            if (!wait_asleep(q_empty, (a.nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) return false;
             mbar_arrive_expect_tx(q_full, TILE_BYTES);
             for (int c = 0; c < 2; ++c)
               tma_load_3d(sQ + c * HALF_BYTES, &mapQ, q_full, a.x.head * DH + c * 64, a.x.qb * BQ,
                           a.x.shard);
             ++units;
           }
-          if (!wait_bounded(k_empty(a.n), ((a.n / NK) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty))
+          if (!wait_asleep(k_empty(a.n), ((a.n / NK) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty))
             return false;
           if (nk != P.debug_drop) {
             mbar_arrive_expect_tx(k_full(a.n), TILE_BYTES);
@@ -323,11 +330,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           a.next(P);
           return true;
         };
-        a.begin(P);
         bool ok = true;
         for (int i = 0; ok && i < NK; ++i) ok = load_k();
         for (w.begin(P); ok && !w.done; w.next(P)) {
-          if (!wait_bounded(v_empty(w.n), ((w.n / NV) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) break;
+          if (!wait_asleep(v_empty(w.n), ((w.n / NV) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) break;
           mbar_arrive_expect_tx(v_full(w.n), TILE_BYTES);
           for (int c = 0; c < 2; ++c)
             tma_load_3d(sV(w.n) + c * HALF_BYTES, &mapV, v_full(w.n), w.x.kvh * DH + c * 64, w.j * BKV,
@@ -347,10 +353,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) {
         // --------------------------------------------------- S = Q K^T issuer
         for (w.begin(P); !w.done; w.next(P)) {
-          if ((w.first && !wait_bounded(q_full, w.nu & 1, abort_flag, P.wait, kErrWaitFull)) ||
-              !wait_bounded(k_full(w.n), (w.n / NK) & 1, abort_flag, P.wait, kErrWaitFull) ||
+          if ((w.first && !wait_asleep(q_full, w.nu & 1, abort_flag, P.wait, kErrWaitFull)) ||
+              !wait_asleep(k_full(w.n), (w.n / NK) & 1, abort_flag, P.wait, kErrWaitFull) ||
               // the buffer's last probabilities have been used
-              (w.n >= NS && !wait_bounded(pv_done(w.n - NS), ((w.n - NS) >> 1) & 1, abort_flag, P.wait,
+              (w.n >= NS && !wait_asleep(pv_done(w.n - NS), ((w.n - NS) / NS) & 1, abort_flag, P.wait,
                                           kErrWaitAttn)))
             break;
           tc_fence_after();
@@ -374,9 +380,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------- O += P V issuer
         for (w.begin(P); !w.done; w.next(P)) {
           if ((w.first && w.nu > 0 &&
-               !wait_bounded(o_empty, (w.nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn)) ||
-              !wait_bounded(v_seen(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull) ||
-              !wait_bounded(p_full(w.n), (w.n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn))
+               !wait_asleep(o_empty, (w.nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn)) ||
+              !wait_asleep(v_seen(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull) ||
+              !wait_asleep(p_full(w.n), (w.n / NS) & 1, abort_flag, P.wait, kErrWaitAttn))
             break;
           tc_fence_after();
           const uint32_t v = sV(w.n), pa = tmem_base + (w.n % NS) * BKV;
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
       // ----------------------------------- values in blocks that a mask cuts
       for (w.begin(P); !w.done; w.next(P)) {
-        bool ok = wait_bounded(v_full(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull);
+        bool ok = wait_asleep(v_full(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (!w.x.t.whole(w.j)) {
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int64_t p_row = -1;       // its row in O [.. * head_dim], -1: not stored
     int64_t p_lse = 0;
     auto wait = [&](uint32_t b, uint32_t parity) {
-      const bool got = wait_bounded(b, parity, abort_flag, P.wait, kErrWaitAttn);
+      const bool got = wait_asleep(b, parity, abort_flag, P.wait, kErrWaitAttn);
       return __all_sync(0xffffffffu, got) != 0;
     };
     auto finish = [&]() {
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           m = m_new;
           if (!w.first && __any_sync(0xffffffffu, grow)) {
             // O is whole once P V of the block before this one is done
-            if (!wait(pv_done(n - 1), ((n - 1) >> 1) & 1)) {
+            if (!wait(pv_done(n - 1), ((n - 1) / NS) & 1)) {
               ok = false;
               break;
             }

@@ -115,6 +115,33 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   }
 }
 
+// The same wait for kernels whose waiting warps share schedulers with busy
+// ones: each try may sleep for up to 20 us in hardware, so that a waiting
+// thread hardly issues (a fifth of the instructions of the attention kernel
+// were those of its waits).
+__device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, volatile int* abort,
+                                            const WaitCtl& w, unsigned code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done != 0) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > w.timeout_ns) {
+      *abort = 1;
+      atomicOr(w.err, code);
+      return false;
+    }
+  }
+}
+
 // Same, but ignores the CTA abort flag: used at teardown to let in-flight
 // asynchronous work (TMA copies, tensor-core ops) finish before the CTA's
 // shared memory and TMEM are released.
