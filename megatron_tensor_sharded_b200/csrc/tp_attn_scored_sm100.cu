@@ -29,7 +29,7 @@
 // group takes over the other's value as soon as it has its block's own
 // maximum, moves it only when it grows by more than 2^8, and hands it on
 // before its exponentials.  A group's sum follows when it next sees a larger
-// maximum; sums and O meet at the unit's end, which each group does after its
+// maximum; sums and O meet at the unit's end, which each group does behind its
 // first block of the next unit.
 //
 // Blocks: each tile walks only the blocks between its rows' least and
@@ -76,6 +76,7 @@ constexpr int BKV = kAttnTile;
 constexpr int NK = 2;                        // ring slots of K
 constexpr int NV = 3;                        // ring slots of V
 constexpr int NS = 3;                        // score buffers in TMEM
+static_assert(NV == NS, "a group finds a block's score buffer and V slot at one index");
 constexpr int TILE_BYTES = 128 * 128 * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;
 constexpr int TILES_BYTES = (1 + NK + NV) * TILE_BYTES;
@@ -127,6 +128,12 @@ __device__ __forceinline__ int32_t unit_of(int32_t r) {
 }
 
 // A walk over the blocks of the CTA's units (units without a block left out).
+// With a bias a unit's last keys come first: near keys weigh most, so the
+// maximum stands after the first block, and O is not rescaled block by block
+// (4096 causal tokens, 64 heads: 375 us, 497 the other way round).  Without one
+// the first keys do: causal rows see a whole block of them, not a corner, and
+// their maximum hardly grows after it (294 us, 344 the other way round).
+template <bool DOWN>
 struct Walk {
   Unit x;
   int32_t r, u, j;   // round, unit, block
@@ -136,7 +143,7 @@ struct Walk {
     for (; u < P.num_units; u = unit_of(++r)) {
       x = decode_unit(P, u);
       if (x.t.jb < x.t.je) {
-        j = x.t.jb;
+        j = DOWN ? x.t.je - 1 : x.t.jb;
         first = true;
         return;
       }
@@ -150,11 +157,11 @@ struct Walk {
     done = false;
     find(P);
   }
-  __device__ __forceinline__ bool last() const { return j + 1 == x.t.je; }
+  __device__ __forceinline__ bool last() const { return DOWN ? j == x.t.jb : j + 1 == x.t.je; }
   __device__ __forceinline__ void next(const ScoredParams& P) {
     ++n;
     first = false;
-    if (++j < x.t.je) return;
+    if (DOWN ? --j >= x.t.jb : ++j < x.t.je) return;
     ++nu;
     u = unit_of(++r);
     find(P);
@@ -167,7 +174,7 @@ struct Walk {
 // with the cap and 2 to 3 without, 9 more where 2^x is there too, and the MUFU
 // unit 8 where it is not.
 template <int MODE>
-constexpr int kPolyPairs = MODE == kCap || MODE == kCapAny ? 1 : 2;
+constexpr int kPolyPairs = MODE == kCap || MODE == kCapAny ? 0 : 2;
 
 // Probabilities of 32 scores: bf16 pairs into pk, fp32 sums into sum2.
 // SCALE: x = v * sc + off, else v holds x itself.
@@ -296,7 +303,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  Walk w;
+  constexpr bool DOWN = MODE == kBias || MODE == kCapAny;
+  Walk<DOWN> w;
   // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
     regs_shrink<64>();
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) {
         // ------------------------------------------------- Q, K and V loads
         // K runs NK blocks ahead of V: a walk each.
-        Walk a;
+        Walk<DOWN> a;
         a.begin(P);
         int64_t nk = 0;
         uint32_t nv = 0, units = 0;
@@ -438,8 +446,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     float m = HAS_MAX ? -INFINITY : 0.0f, l = 0.0f;
     bool poison = false, lost = false;
-    int2 seen = make_int2(0, -1);
-    float slope2 = 0.0f;
     // the unit whose end is still to be done
     bool pending = false;
     uint32_t p_nu = 0;
@@ -490,28 +496,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       return true;
     };
-    for (w.begin(P); !w.done; w.next(P)) {
-      const uint32_t n = w.n;
-      const int32_t q = w.x.qb * BQ + row;
-      if (w.first) {
-        seen = row_span(P.mask, q, P.T, P.causal);
-        if (MODE == kBias || MODE == kCapAny)
-          slope2 = P.slopes != nullptr
-                       ? 1.4426950408889634f * P.slopes[w.x.shard * P.hq + w.x.head]
-                       : 0.0f;
-      }
-      if (static_cast<int>(n & 1) == g) {
-        // (behind the unit's first block the previous unit's end must be done:
-        // the values' products wait for it, and a rescaled O for them)
-        if (pending && !w.first && !finish()) break;
-        const uint32_t tS = tmem_base + lane_off + (n % NS) * BKV + half * 64;
-        const int32_t key0 = w.j * BKV + half * 64, rl = seen.x - key0, rh = seen.y - key0;
-        const bool whole = w.x.t.whole(w.j);
-        ok = wait(s_full(n), (n / NS) & 1);
-        if (!ok) break;
+    // Blocks are counted through the CTA's units; a group's are every second
+    // one, so from one to the next the score buffer moves on by two.
+    uint32_t slot = g, phase = 0;      // n % NS and (n / NS) & 1 of the group's next block
+    uint32_t turn = 0;                 // (n >> 1) & 1
+    uint32_t nu = 0, parity0 = 0;      // units, and the parity of a unit's first block
+    bool started = g == 1;             // a block came before (of either group)
+    int32_t r = 0;
+    for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
+      const Unit x = decode_unit(P, u);
+      const int32_t blocks = x.t.je - x.t.jb;
+      if (blocks <= 0) continue;
+      const int32_t q = x.qb * BQ + row;
+      const int2 seen = row_span(P.mask, q, P.T, P.causal);
+      float slope2 = 0.0f;
+      if (MODE == kBias || MODE == kCapAny)
+        slope2 = P.slopes != nullptr ? 1.4426950408889634f * P.slopes[x.shard * P.hq + x.head] : 0.0f;
+      for (int32_t i = (static_cast<uint32_t>(g) ^ parity0) & 1; i < blocks; i += 2) {
+        // (a group that enters the unit with its second block does the previous
+        // unit's end first, since the first block's P V waits for it; with a
+        // maximum its block comes first, and measured 7% better)
+        if (!HAS_MAX && pending && i > 0 && !finish()) {
+          ok = false;
+          break;
+        }
+        const int32_t j = DOWN ? x.t.je - 1 - i : x.t.jb + i;
+        const uint32_t tS = tmem_base + lane_off + slot * BKV + half * 64;
+        const bool whole = x.t.whole(j);
+        const int32_t key0 = j * BKV + half * 64;
+        if (!wait(s_full(slot), phase)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const float dist0 = static_cast<float>(key0 - q);
-        const int side = w.j * BKV + BKV - 1 <= w.x.qb * BQ ? -1 : w.j * BKV >= w.x.qb * BQ + BQ - 1 ? 1 : 0;
+        const int32_t rl = seen.x - key0, rh = seen.y - key0;
+        float dist0 = 0.0f;
+        int side = 0;
+        if (MODE == kBias || MODE == kCapAny) {
+          dist0 = static_cast<float>(key0 - q);
+          side = j * BKV + BKV - 1 <= x.qb * BQ ? -1 : j * BKV >= x.qb * BQ + BQ - 1 ? 1 : 0;
+        }
         uint64_t sum2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
         // (loops kept rolled: the instruction cache holds one chunk's code)
         if (HAS_MAX) {
@@ -528,20 +552,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               acc[0] = max3_nan(acc[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
               acc[1] = max3_nan(acc[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
             }
-            if (MODE != kPlain) tmem_st_32x32b_x32(tS + c * 32, v);
+            if (MODE == kCapAny) tmem_st_32x32b_x32(tS + c * 32, v);   // (else computed again below)
           }
-          if (MODE != kPlain) tmem_st_wait();
+          if (MODE == kCapAny) tmem_st_wait();
           float m_cand = max3_nan(acc[0], acc[1], acc[1]);
           // the other group's maximum first: its arrival also says that this
           // group's last exchange has been read
-          if (n > 0 && !wait(m_ready(n - 1), ((n - 1) >> 1) & 1)) {
+          if (started && !wait(m_ready(g ^ 1), turn ^ (g ^ 1))) {
             ok = false;
             break;
           }
-          const float m_prev = w.first ? -INFINITY : run_m[(g ^ 1) * BQ + row];
+          const float m_prev = i == 0 ? -INFINITY : run_m[(g ^ 1) * BQ + row];
           xch[part * BQ + row] = m_cand;
-          mbar_arrive(x_full(n));
-          if (!wait(x_full(n), (n >> 1) & 1)) {
+          mbar_arrive(x_full(g));
+          if (!wait(x_full(g), turn)) {
             ok = false;
             break;
           }
@@ -551,12 +575,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const bool grow = !(m_cand <= m_prev + RESCALE_LOG2);   // NaN too: it then stays
           const float m_new = grow ? m_cand : m_prev;
           if (half == 0) run_m[g * BQ + row] = m_new;
-          mbar_arrive(m_ready(n));
+          mbar_arrive(m_ready(g));
           if (m != m_new) l *= ex2(m - m_new);
           m = m_new;
-          if (!w.first && __any_sync(0xffffffffu, grow)) {
-            // O is whole once P V of the block before this one is done
-            if (!wait(pv_done(n - 1), ((n - 1) / NS) & 1)) {
+          if (i > 0 && __any_sync(0xffffffffu, grow)) {
+            // O is whole once P V of the block before this one is done, which
+            // itself waits for the end of the previous unit
+            const uint32_t before = slot == 0 ? NS - 1 : slot - 1;
+            if ((pending && !finish()) || !wait(pv_done(before), slot == 0 ? phase ^ 1u : phase)) {
               ok = false;
               break;
             }
@@ -581,54 +607,58 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_ld_32x32b_x32(tS + c * 32, v);
           tmem_ld_wait();
           if (MODE == kPlain && !whole) mask_chunk(v, rl - c * 32, rh - c * 32);
-          if (MODE == kCap)
-            score_chunk<MODE>(v, S, slope2, dist0, side, whole, rl - c * 32, rh - c * 32, lost);
+          if (MODE == kCap || MODE == kBias)
+            score_chunk<MODE>(v, S, slope2, dist0 + c * 32.0f, side, whole, rl - c * 32,
+                              rh - c * 32, lost);
           exp_chunk<kPolyPairs<MODE>, HAS_MAX>(v, f2_pack(scale, scale), f2_pack(off, off), sum2, pk);
           tmem_st_32x32b_x16(tS + c * 16, pk);
         }
         tmem_st_wait();
         if (!whole) {   // keys in sight whose value is not finite
-          if (!wait(v_seen(n), (n / NV) & 1)) {
+          if (!wait(v_seen(slot), phase)) {
             ok = false;
             break;
           }
-          const volatile uint32_t* b = bad + (n % NV) * 4 + half * 2;
+          const volatile uint32_t* b = bad + slot * 4 + half * 2;
           if (b[0] | b[1]) {
             for (int e = 0; e < 64; ++e)
               poison |= e >= rl && e < rh && ((b[e >> 5] >> (e & 31)) & 1);
           }
         }
         tc_fence_before();
-        mbar_arrive(p_full(n));
+        mbar_arrive(p_full(slot));
         float s0, s1, s2, s3;
         f2_unpack(sum2[0], s0, s1);
         f2_unpack(sum2[1], s2, s3);
         l += (s0 + s1) + (s2 + s3);
+        slot += 2;
+        if (slot >= NS) {
+          slot -= NS;
+          phase ^= 1u;
+        }
+        turn ^= 1u;
+        started = true;
         if (pending && !finish()) {
           ok = false;
           break;
         }
       }
-      if (w.last()) {
-        if (pending && !finish()) {
-          ok = false;
-          break;
-        }
-        // this unit's sums; its end follows
-        volatile float* e = ends + (w.nu & 1) * 3 * 4 * BQ + row;
-        e[part * BQ] = lost ? NAN : l;
-        if (HAS_MAX) e[(4 + part) * BQ] = m;
-        e[(8 + part) * BQ] = poison ? 1.0f : 0.0f;
-        mbar_arrive(e_full);
-        pending = true;
-        p_nu = w.nu;
-        const bool store = q < P.T && seen.y >= 0;   // rows of no document stay as they were
-        p_row = store ? ((static_cast<int64_t>(w.x.shard) * P.T + q) * P.hq + w.x.head) * DH : -1;
-        p_lse = (static_cast<int64_t>(w.x.shard) * P.hq + w.x.head) * P.T + q;
-        m = HAS_MAX ? -INFINITY : 0.0f;
-        l = 0.0f;
-        poison = lost = false;
-      }
+      if (!ok || (pending && !finish())) break;
+      parity0 ^= blocks & 1;
+      // this unit's sums; its end follows
+      volatile float* e = ends + (nu & 1) * 3 * 4 * BQ + row;
+      e[part * BQ] = lost ? NAN : l;
+      if (HAS_MAX) e[(4 + part) * BQ] = m;
+      e[(8 + part) * BQ] = poison ? 1.0f : 0.0f;
+      mbar_arrive(e_full);
+      pending = true;
+      p_nu = nu++;
+      const bool store = q < P.T && seen.y >= 0;   // rows of no document stay as they were
+      p_row = store ? ((static_cast<int64_t>(x.shard) * P.T + q) * P.hq + x.head) * DH : -1;
+      p_lse = (static_cast<int64_t>(x.shard) * P.hq + x.head) * P.T + q;
+      m = HAS_MAX ? -INFINITY : 0.0f;
+      l = 0.0f;
+      poison = lost = false;
     }
     if (ok && pending) finish();
   }
