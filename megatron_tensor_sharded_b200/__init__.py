@@ -239,12 +239,29 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = None   # () -> address of torch's current stream on its current device
+
+
+def _find_raw_stream():
+    """The current stream's address by torch's own short way (0.2 us; the
+    stream object of the public call takes 1 us, asking whether a GPU is there
+    3 us more), or by the public one where that is missing."""
+    import torch
+    c = torch._C
+    if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+        return lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return lambda: torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        if torch.cuda.is_available() and torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
-        return None
+        if _raw_stream is None:
+            import torch
+            if not torch.cuda.is_initialized():
+                return None
+            _raw_stream = _find_raw_stream()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -672,11 +672,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // ------------------------------------------------------------- mask's plan
 // One CTA per tile of 128 rows: each row finds its document (binary search of
-// the offsets) and writes its visible keys; the tile's summary follows.
+// the offsets) and writes the keys it sees and the queries that see it; the
+// tile's summary as queries and as keys follows.
 __global__ void __launch_bounds__(kAttnTile)
-    mask_rows_kernel(const int32_t* __restrict__ off, int32_t n_docs,
+    mask_plan_kernel(const int32_t* __restrict__ off, int32_t n_docs,
                      const int32_t* __restrict__ prefix, int32_t causal, MaskPlan plan, int32_t T) {
-  __shared__ int32_t red[4][kAttnTile / 32];
+  __shared__ int32_t red[6][kAttnTile / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int32_t t = blockIdx.x * kAttnTile + threadIdx.x;
@@ -708,49 +709,24 @@ __global__ void __launch_bounds__(kAttnTile)
     plan.keys[t] = by;
   }
   const bool in = hi >= 0;
-  int32_t v[4] = {in ? lo : INT_MAX, in ? hi : 0, t < T ? lo : 0, t < T ? hi : INT_MAX};
+  // least and greatest of each, as minima
+  int32_t v[6] = {in ? lo : INT_MAX, in ? -hi : 0,  t < T ? -lo : 0,
+                  t < T ? hi : INT_MAX, in ? by.x : INT_MAX, in ? -by.y : 0};
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) {
-    v[0] = min(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-    v[1] = max(v[1], __shfl_xor_sync(0xffffffffu, v[1], o));
-    v[2] = max(v[2], __shfl_xor_sync(0xffffffffu, v[2], o));
-    v[3] = min(v[3], __shfl_xor_sync(0xffffffffu, v[3], o));
+  for (int i = 0; i < 6; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v[i] = min(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
+    if (threadIdx.x % 32 == 0) red[i][threadIdx.x / 32] = v[i];
   }
-  if (threadIdx.x % 32 == 0)
-    for (int i = 0; i < 4; ++i) red[i][threadIdx.x / 32] = v[i];
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kAttnTile / 32; ++w) {
-      v[0] = min(v[0], red[0][w]);
-      v[1] = max(v[1], red[1][w]);
-      v[2] = max(v[2], red[2][w]);
-      v[3] = min(v[3], red[3][w]);
-    }
-    plan.q_tiles[blockIdx.x] = make_int4(v[0], v[1], v[2], v[3]);
-  }
-}
-
-// The query tiles that may see a key of each tile of 128 keys: one warp a
-// key tile.
-__global__ void __launch_bounds__(kAttnTile) mask_tiles_kernel(MaskPlan plan, int32_t tiles) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int32_t j = blockIdx.x * (kAttnTile / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (j >= tiles) return;
-  int32_t first = INT_MAX, last = -1;
-  for (int32_t i = lane; i < tiles; i += 32) {
-    const int4 s = plan.q_tiles[i];
-    if (s.x < s.y && s.x / kAttnTile <= j && (s.y - 1) / kAttnTile >= j) {
-      first = min(first, i);
-      last = max(last, i);
-    }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) {
-    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-    last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+    for (int i = 0; i < 6; ++i)
+      for (int w = 1; w < kAttnTile / 32; ++w) v[i] = min(v[i], red[i][w]);
+    plan.q_tiles[blockIdx.x] = make_int4(v[0], -v[1], -v[2], v[3]);
+    plan.k_tiles[blockIdx.x] = v[4] < -v[5] ? make_int2(v[4] / kAttnTile, (-v[5] - 1) / kAttnTile + 1)
+                                            : make_int2(0, 0);
   }
-  if (lane == 0) plan.k_tiles[j] = last < 0 ? make_int2(0, 0) : make_int2(first, last + 1);
 }
 
 template <int MODE>
@@ -788,13 +764,9 @@ cudaError_t launch_attention_mask(const LaunchCtx& c, const int32_t* off, int n_
                                   const int32_t* prefix, bool causal, void* mask, int64_t T) {
   const MaskPlan plan = mask_plan(mask, T);
   const int32_t tiles = ceil_div(T, kAttnTile);
-  cudaError_t e = launch_pdl(mask_rows_kernel, dim3(tiles), dim3(kAttnTile), 0, c.stream, off,
-                             static_cast<int32_t>(n_docs), prefix, causal ? 1 : 0, plan,
-                             static_cast<int32_t>(T));
-  note_launch();
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(mask_tiles_kernel, dim3(ceil_div(tiles, kAttnTile / 32)), dim3(kAttnTile), 0,
-                 c.stream, plan, tiles);
+  const cudaError_t e = launch_pdl(mask_plan_kernel, dim3(tiles), dim3(kAttnTile), 0, c.stream, off,
+                                   static_cast<int32_t>(n_docs), prefix, causal ? 1 : 0, plan,
+                                   static_cast<int32_t>(T));
   note_launch();
   return e;
 }
