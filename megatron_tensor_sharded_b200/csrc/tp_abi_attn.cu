@@ -178,9 +178,14 @@ tp_status score_call(ScoreCall* a, int64_t T, int p, int n_heads, int n_kv_heads
   return TP_OK;
 }
 
-// Backward workspace: D, one number a query row and head.
-size_t score_bwd_ws(const ScoreCall& a) {
-  return align256(static_cast<size_t>(a.T) * a.p * a.hq * 4);
+// Backward workspace: D, a number a query row and head, a byte a key row and
+// head, then the partial dK and dV.  (The mask and the causal option do not
+// change its size.)
+size_t score_delta_ws(const ScoreCall& a) { return align256(static_cast<size_t>(a.T) * a.p * a.hq * 4); }
+size_t score_bad_ws(const ScoreCall& a) { return align256(static_cast<size_t>(a.T) * a.p * a.hkv); }
+size_t score_bwd_ws(ScoreCall a) {
+  a.causal = false;
+  return score_delta_ws(a) + score_bad_ws(a) + align256(score_dkv_bytes(a));
 }
 
 // Sizes and options of a decode call into `a` (its T is the batch).
@@ -490,6 +495,8 @@ tp_status tp_attention_scored_backward(const void* Q, const void* K, const void*
   a.dK = dK;
   a.dV = dV;
   a.delta = static_cast<float*>(workspace);
+  a.k_bad = static_cast<uint8_t*>(workspace) + score_delta_ws(a);
+  a.part = reinterpret_cast<float*>(a.k_bad + score_bad_ws(a));
   LaunchCtx c{};
   TP_TRY(make_launch_ctx(stream, true, &c));
   return launch_attention_scored_bwd(c, a);

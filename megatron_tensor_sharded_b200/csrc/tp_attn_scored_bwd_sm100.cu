@@ -1,15 +1,17 @@
-// Backward of scored attention (sm_100a): three launches.
+// Backward of scored attention (sm_100a): four launches.
 //
 // With P = exp(z - LSE), D_i = sum_d dO_id O_id and t the cap's tanh,
 //   dV_j = sum_i P_ij dO_i,   dS_ij = P_ij (dO_i.v_j - D_i) (1 - t_ij^2),
 //   dQ_i = scale sum_j dS_ij k_j,   dK_j = scale sum_i dS_ij q_i,
 // dK and dV summed over the query heads that share a key/value head.
 //
-// 1. score_delta_kernel: D, one pass over O and dO (HBM-bound).
+// 1. score_delta_kernel: D, and which rows of Q, dO and K hold infinities or
+//    NaN, one pass over O, dO, Q and K (HBM-bound).
 // 2. tc_scored_dkv_kernel: a unit is (shard, key/value head, 128 keys) and
 //    walks every query tile that sees them, for every query head of the
 //    group: dK and dV stay in TMEM from the first to the last, so the sum
-//    over heads costs nothing and has a fixed order.
+//    over heads costs nothing and has a fixed order; dkv_join_kernel adds what
+//    units on several CTAs left.
 // 3. tc_scored_dq_kernel: a unit is (shard, query head, 128 queries) and walks
 //    its key blocks with dQ in TMEM.
 // Scores and probabilities are recomputed in both: seven products a tile
@@ -30,8 +32,12 @@
 // S^T, the next S^T waited for dV: 4150 clocks a step against 2048 of
 // products.)
 //
+// A query that sees one key has P = 1 and dS = 0 exactly; dP - D leaves the
+// rounding of two sums there, so w is set to 0 (times 0: a NaN stays).
+//
 // Masks, and rows that hold infinities or NaN outside what is seen, as in the
-// forward kernel; here the tiles of Q and dO (dkv) and of K (dq) are looked at.
+// forward kernel; here rows of Q and dO (dkv) and of K (dq) that the first kernel
+// marked are set to 0 in tiles that a mask cuts.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -72,16 +78,25 @@ constexpr uint32_t IDESC_KN = idesc_bf16_f32(BT, DH, 0, 1);   // A in TMEM, B ro
 template <bool CAP>
 constexpr int kPolyPairs = CAP ? 0 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kUnitCost = 2;                  // of a dkv unit beside its steps, in steps
+constexpr int kWholeUnits = 6;                // units a CTA from which none is cut
+constexpr int kCut = 1, kFirst = 2, kLast = 4, kEnd = 8;   // a step: cut by a mask; its unit's; the share's last
+constexpr int PART_FLOATS = 2 * BT * DH;      // dV and dK of a key tile
 
 struct BwdParams {
   int32_t T, p, hq, hkv, group, tiles, num_units, causal;
+  int32_t whole;            // dkv: units are not cut
   MaskPlan mask;
   ScoreConsts s;
   float neg_inv_cap2;       // -(cap log2 e)^-2: 1 - tanh^2 = 1 + z^2 times it
   const float* slopes;
   const float* LSE;
   const float* delta;
+  const uint8_t* k_bad;     // rows of K that hold an infinity or a NaN
   __nv_bfloat16 *dQ, *dK, *dV;
+  float* part;              // dkv: [cta][slot][dV, dK][128][head_dim] of units that lie on several CTAs
+  int4* cuts;               // dkv: where each CTA's share begins {key tile, head, step, steps of the unit}
+  int64_t* total;           // dkv: steps of all units
   WaitCtl wait;
   int64_t debug_drop;
 };
@@ -93,21 +108,21 @@ __device__ __forceinline__ int32_t unit_of(int32_t r) {
 
 // A product of two shared-memory tiles along head_dim: D = A B^T.
 __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b) {
+  const uint32_t al = desc_lo(a, 16), bl = desc_lo(b, 16);
 #pragma unroll
   for (int kk = 0; kk < DH / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-    tc_mma_f16(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), IDESC_KK,
-               kk > 0 ? 1u : 0u);
+    const uint32_t off = desc_step((kk >> 2) * HALF_BYTES + (kk & 3) * 32);
+    tc_mma_f16_lo(d, al + off, bl + off, IDESC_KK, kk > 0 ? 1u : 0u);
   }
 }
 // D (+)= A B with A (bf16, each column quarter at its 32 columns' start) in
 // TMEM and B's 128 rows the contraction.
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  const uint32_t bl = desc_lo(b, HALF_BYTES);
 #pragma unroll
   for (int kk = 0; kk < BT / 16; ++kk)
-    tc_mma_f16_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8,
-                  smem_desc_sw128(b + kk * 16 * 128, HALF_BYTES, 1024), IDESC_KN,
-                  (add || kk > 0) ? 1u : 0u);
+    tc_mma_f16_ts_lo(d, a + (kk >> 1) * 32 + (kk & 1) * 8, bl + desc_step(kk * 16 * 128), IDESC_KN,
+                     (add || kk > 0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -117,7 +132,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 }
 
 // 32 raw products -> P as bf16 pairs in pk and w = P (1 - tanh^2).  nl(e):
-// -LSE log2 e of columns e and e + 1; seen(e): whether the pair counts.
+// -LSE log2 e of columns e .. e + 3; seen(e): whether the pair counts.
 template <bool CAP, bool BIAS, typename NegLse, typename Seen>
 __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], uint32_t (&pk)[16],
                                            const BwdParams& P, float slope2, float dist0, int side,
@@ -133,10 +148,12 @@ __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], ui
   }
   if (BIAS) bias_chunk<!CAP>(v, P.s.scale_log2, slope2, dist0, side);
   const uint64_t sc2 = f2_pack(P.s.scale_log2, P.s.scale_log2);
+  uint64_t n[2];
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
+    if (e % 4 == 0) nl(e, n[0], n[1]);
     uint64_t x = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-    x = CAP || BIAS ? f2_add(x, nl(e)) : f2_fma(x, sc2, nl(e));
+    x = CAP || BIAS ? f2_add(x, n[(e / 2) & 1]) : f2_fma(x, sc2, n[(e / 2) & 1]);
     float a, b;
     if ((e / 2) % 8 < kPolyPairs<CAP>) {
       f2_unpack(exp2_poly5<true>(x), a, b);
@@ -170,13 +187,15 @@ __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], ui
   }
 }
 
-// 32 products dP -> dS = w (dP - D) as bf16 pairs; nd(e): -D of columns e, e + 1.
+// 32 products dP -> dS = w (dP - D) as bf16 pairs; nd(e): -D of columns e .. e + 3.
 template <typename NegDelta, typename Seen>
 __device__ __forceinline__ void grad_chunk(uint32_t (&v)[32], const float (&w)[32],
                                            uint32_t (&pk)[16], bool cut, NegDelta nd, Seen seen) {
+  uint64_t n[2];
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    const uint64_t x = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), nd(e));
+    if (e % 4 == 0) nd(e, n[0], n[1]);
+    const uint64_t x = f2_add(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), n[(e / 2) & 1]);
     float a, b;
     f2_unpack(f2_mul(x, f2_pack(w[e], w[e + 1])), a, b);
     v[e] = __float_as_uint(a);
@@ -209,46 +228,101 @@ __device__ __forceinline__ void store_part_row(uint32_t taddr, float f, bool sto
   }
 }
 
-__device__ __forceinline__ float lds(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint64_t lds2(uint32_t addr) {
-  uint64_t v;
-  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
-  return v;
+__device__ __forceinline__ void lds4(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 __device__ __forceinline__ void sts(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// The same columns in fp32.
+__device__ __forceinline__ void keep_part_row(uint32_t taddr, float f, float* dst) {
+  uint32_t v[32];
+  tmem_ld_32x32b_x32(taddr, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    *reinterpret_cast<float4*>(dst + g * 4) =
+        make_float4(__uint_as_float(v[g * 4]) * f, __uint_as_float(v[g * 4 + 1]) * f,
+                    __uint_as_float(v[g * 4 + 2]) * f, __uint_as_float(v[g * 4 + 3]) * f);
+}
+
 // ------------------------------------------------------------------ delta
-// D[shard][head][t] = sum over the head of dO * O: 16 lanes a row, four rows of
-// each lane loaded together.
+// D[shard][head][t] = sum over the head of dO * O, NaN where the query's row of
+// Q holds an infinity or a NaN (one of dO makes D one by itself); and for each
+// row of K whether it does.  The kernels below look at a row in shared memory
+// only where these say so.  (Looked at there in every tile that a mask cuts,
+// they bound the backward of short documents: dK and dV of 1999 tokens in five
+// took 149 us instead of 109.)
+// 16 lanes a row, four rows of each lane loaded together.
 constexpr int DELTA_ROWS = 64;   // rows of a CTA
+// 0 if the eight values are finite, else NaN
+__device__ __forceinline__ float zero_or_nan(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  __nv_bfloat162 a = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 x;
+    memcpy(&x, &w[i], 4);
+    a = __hfma2(x, __floats2bfloat162_rn(0.0f, 0.0f), a);
+  }
+  return __low2float(a) + __high2float(a);
+}
+// element of [shard][heads][T] that row [shard][t][head] is
+__device__ __forceinline__ int64_t by_head(int64_t row, int64_t rows, int32_t T, int32_t heads) {
+  int64_t st, shard;   // st = shard * T + t
+  if (rows >> 31) {
+    st = row / heads;
+    shard = st / T;
+  } else {
+    st = static_cast<uint32_t>(row) / static_cast<uint32_t>(heads);
+    shard = static_cast<uint32_t>(st) / static_cast<uint32_t>(T);
+  }
+  return (shard * heads + (row - st * heads)) * T + (st - shard * T);
+}
+__device__ __forceinline__ void load_rows(uint4 (&v)[4], const __nv_bfloat16* x, int64_t row0,
+                                          int64_t rows, int lane) {
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int64_t row = row0 + n * 16;
+    v[n] = make_uint4(0, 0, 0, 0);
+    if (row < rows) v[n] = *reinterpret_cast<const uint4*>(x + row * DH + lane * 8);
+  }
+}
+// blocks [0, q_blocks): rows of Q; the others: of K
 __global__ void __launch_bounds__(256)
     score_delta_kernel(const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
-                       float* __restrict__ delta, int64_t rows, int32_t T, int32_t hq) {
+                       const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ K,
+                       float* __restrict__ delta, uint8_t* __restrict__ k_bad, uint32_t q_blocks,
+                       int64_t shard_rows, int32_t T, int32_t hq, int32_t hkv) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * DELTA_ROWS + threadIdx.x / 16;   // [shard][t][head]
   const int lane = threadIdx.x % 16;
-  uint4 a[4], b[4];
+  if (blockIdx.x >= q_blocks) {
+    const int64_t rows = shard_rows * hkv;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x - q_blocks) * DELTA_ROWS + threadIdx.x / 16;
+    uint4 k[4];
+    load_rows(k, K, row0, rows, lane);
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int64_t row = row0 + n * 16;
-    a[n] = b[n] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      a[n] = *reinterpret_cast<const uint4*>(O + row * DH + lane * 8);
-      b[n] = *reinterpret_cast<const uint4*>(dO + row * DH + lane * 8);
+    for (int n = 0; n < 4; ++n) {
+      float z = zero_or_nan(k[n]);
+#pragma unroll
+      for (int o = 8; o > 0; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
+      const int64_t row = row0 + n * 16;
+      if (lane == 0 && row < rows) k_bad[by_head(row, rows, T, hkv)] = z != z;
     }
+    return;
   }
+  const int64_t rows = shard_rows * hq;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * DELTA_ROWS + threadIdx.x / 16;
+  uint4 a[4], b[4], q[4];
+  load_rows(a, O, row0, rows, lane);
+  load_rows(b, dO, row0, rows, lane);
+  load_rows(q, Q, row0, rows, lane);
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const int64_t row = row0 + n * 16;
     const uint32_t x[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, y[4] = {b[n].x, b[n].y, b[n].z, b[n].w};
-    float s = 0.0f;
+    float s = zero_or_nan(q[n]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       s += __uint_as_float(x[i] << 16) * __uint_as_float(y[i] << 16);
@@ -256,40 +330,156 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int o = 8; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (row < rows && lane == 0) {
-      int64_t st, shard;   // st = shard * T + t
-      if (rows >> 31) {
-        st = row / hq;
-        shard = st / T;
-      } else {
-        st = static_cast<uint32_t>(row) / static_cast<uint32_t>(hq);
-        shard = static_cast<uint32_t>(st) / static_cast<uint32_t>(T);
-      }
-      delta[(shard * hq + (row - st * hq)) * T + (st - shard * T)] = s;
-    }
+    const int64_t row = row0 + n * 16;
+    if (lane == 0 && row < rows) delta[by_head(row, rows, T, hq)] = s;
   }
 }
 
 // ---------------------------------------------------------------- dK and dV
-struct KeyUnit {
-  int32_t shard, kvh, kb, ia, ib;   // query tiles [ia, ib)
-};
-__device__ __forceinline__ KeyUnit key_unit(const BwdParams& P, int32_t u) {
-  KeyUnit x;
-  const int32_t heads = P.p * P.hkv;
-  x.kb = u / heads;                 // causal: the first keys are seen by most
-  const int32_t hh = u % heads;
-  x.shard = hh / P.hkv;
-  x.kvh = hh % P.hkv;
-  if (P.mask.rows != nullptr) {
-    const int2 t = P.mask.k_tiles[x.kb];
-    x.ia = t.x;
-    x.ib = t.y;
-  } else {
-    x.ia = P.causal ? x.kb : 0;
-    x.ib = P.tiles;
+// Units, ordered by key tile (causal: the first keys are seen by most) and then
+// (shard, key/value head), lie behind one another on a line of steps (a query
+// head's query tile each, and kUnitCost for the loads and stores of the unit);
+// every CTA gets an equal stretch of it.  A unit that the end of a stretch cuts
+// leaves fp32 partials (slot 0: the part that a CTA finds begun, slot 1: the
+// one that it begins), which dkv_join_kernel adds in the order of the CTAs.
+// Handed out whole instead, units leave SMs idle where there are few of them or
+// where documents make them differ: 369 us for the whole backward against 244
+// for 1999 tokens of five documents, 64 query and 8 key/value heads.  But a cut
+// costs a store, a load and a sum of 128 KB, and where the CTAs take many units
+// each, in turns from the two ends, their sums are even anyway: P.whole
+// (kWholeUnits a CTA, no mask): 648 us against 616 for 4096 tokens and 32 heads.
+__device__ __forceinline__ int2 key_tiles(const BwdParams& P, int32_t kb) {
+  if (P.mask.rows != nullptr) return P.mask.k_tiles[kb];
+  return make_int2(P.causal ? kb : 0, P.tiles);
+}
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t c, int64_t ctas) {
+  return total * c / ctas;
+}
+
+__device__ __forceinline__ int4 lds_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts4(uint32_t addr, int a, int b, int c, int d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+struct Segment {
+  int32_t kb, hh, shard, kvh, ia, ni;   // query tiles [ia, ia + ni)
+  int32_t s0, s1, steps;                // steps [s0, s1) of the unit's
+  uint32_t left;                        // of the CTA's share, from s0 on
+  int32_t turn;
+  __device__ __forceinline__ uint32_t cost() const { return static_cast<uint32_t>(steps + kUnitCost - s0); }
+  __device__ __forceinline__ void set(const BwdParams& P) {
+    const int2 t = key_tiles(P, kb);
+    ia = t.x;
+    ni = t.y - t.x;
+    steps = P.group * ni;
+    shard = hh / P.hkv;
+    kvh = hh - shard * P.hkv;
+    s1 = left < static_cast<uint32_t>(steps - s0) ? s0 + static_cast<int32_t>(left) : steps;
   }
-  return x;
+  // start: {kb, hh, s0, left}
+  __device__ __forceinline__ void begin(const BwdParams& P, int4 start) {
+    kb = start.x;
+    hh = start.y;
+    s0 = start.z;
+    left = static_cast<uint32_t>(start.w);
+    turn = 0;
+    if (P.whole) {
+      take(P);
+      return;
+    }
+    if (left > 0) set(P);
+  }
+  __device__ __forceinline__ bool last() const { return left <= cost(); }
+  // P.whole: the CTA's turn-th unit
+  __device__ __forceinline__ void take(const BwdParams& P) {
+    const int32_t u = unit_of(turn), heads = P.p * P.hkv;
+    left = 0;
+    if (u >= P.num_units) return;
+    kb = u / heads;
+    hh = u - kb * heads;
+    s0 = 0;
+    left = 0x7fffffffu;
+    set(P);
+    if (unit_of(turn + 1) >= P.num_units) left = cost();
+  }
+  __device__ __forceinline__ void next(const BwdParams& P) {
+    if (P.whole) {
+      ++turn;
+      take(P);
+      return;
+    }
+    if (last()) {
+      left = 0;
+      return;
+    }
+    left -= cost();
+    s0 = 0;
+    if (++hh == P.p * P.hkv) {
+      hh = 0;
+      do {
+        if (++kb >= P.tiles) {   // (a mask that is none)
+          left = 0;
+          return;
+        }
+        const int2 t = key_tiles(P, kb);
+        ni = t.y - t.x;
+      } while (ni <= 0);
+    }
+    set(P);
+  }
+  __device__ __forceinline__ bool whole() const { return s0 == 0 && s1 == steps; }
+};
+
+// This CTA's share of the line, by one warp; -> {kb, hh, s0, left} (lane 0).
+__device__ __forceinline__ int4 find_share(const BwdParams& P, int lane) {
+  const int64_t heads = static_cast<int64_t>(P.p) * P.hkv;
+  int64_t total = 0;
+  for (int32_t k0 = 0; k0 < P.tiles; k0 += 32) {
+    const int2 t = k0 + lane < P.tiles ? key_tiles(P, k0 + lane) : make_int2(0, 0);
+    int64_t x = t.y > t.x ? heads * (static_cast<int64_t>(P.group) * (t.y - t.x) + kUnitCost) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    total += x;
+  }
+  const int64_t w0 = share_of(total, blockIdx.x, gridDim.x);
+  const int64_t w1 = share_of(total, blockIdx.x + 1, gridDim.x);
+  int4 found = make_int4(0, 0, 0, 0);
+  int64_t done = 0;
+  for (int32_t k0 = 0; k0 < P.tiles && done <= w0 && w0 < w1; k0 += 32) {
+    const int2 t = k0 + lane < P.tiles ? key_tiles(P, k0 + lane) : make_int2(0, 0);
+    const int64_t steps = t.y > t.x ? static_cast<int64_t>(P.group) * (t.y - t.x) + kUnitCost : 0;
+    int64_t x = heads * steps;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int64_t before = done + x - heads * steps, at = w0 - before;
+    const bool mine = steps > 0 && at >= 0 && at < heads * steps;
+    const int32_t hh = mine ? static_cast<int32_t>(at / steps) : 0;
+    const int32_t s0 = mine ? static_cast<int32_t>(at - hh * steps) : 0;
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    if (who != 0) {
+      const int src = __ffs(who) - 1;
+      found = make_int4(k0 + src, __shfl_sync(0xffffffffu, hh, src), __shfl_sync(0xffffffffu, s0, src),
+                        static_cast<int32_t>(w1 - w0));
+    }
+    done += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) {
+    Segment x;
+    x.begin(P, found);
+    if (x.left > 0 && x.s0 >= x.steps) x.next(P);   // begins behind a unit's steps
+    found = make_int4(x.kb, x.hh, x.s0, static_cast<int32_t>(x.left));
+    P.cuts[blockIdx.x] = x.left > 0 ? make_int4(x.kb, x.hh, x.s0, x.steps) : make_int4(0, 0, 0, 0);
+    if (blockIdx.x == 0) *P.total = total;
+  }
+  return found;
 }
 
 template <bool CAP, bool BIAS>
@@ -325,25 +515,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain = smem_u32(&bars[20]);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * 21);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile uint32_t* const cut_flag = tmem_slot + 2;   // [NB]: the step's tile is cut by a mask
   volatile uint32_t* const bad = tmem_slot + 4;        // [NB][4]: its rows of dO or Q that are not finite
   // [3][4]: keys that see one, by unit number mod 3 (set by any column
   // quarter's thread of the key, read by all at the unit's end; cleared two
   // units ahead, when the last reader of the slot has moved on)
   uint32_t* const hit = tmem_slot + 4 + NB * 4;
+  // what warps 2 and 3 tell the arithmetic warps, who then need not keep it:
+  // [NB] of each step {query tile, kCut | ... | kEnd, slope log2 e, -}, and
+  // [4] of each unit {key tile, head, where its sums go: -1 dK and dV, else the
+  // slot of the partials, -}
+  const uint32_t about = smem_u32(ctrl) + 320, about_unit = about + NB * 16;
+  // [NB][4]: its queries that see one key only
+  volatile uint32_t* const lone = reinterpret_cast<volatile uint32_t*>(ctrl + 464);
+  const uint32_t share = smem_u32(ctrl) + 448;   // find_share's {kb, hh, s0, left}
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
-    // (empty: the MMA thread's commit, warps 2 and 3)
     for (int s = 0; s < NA; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 3);
+      mbar_init(q_empty(s), 1);
     }
     for (int s = 0; s < NB; ++s) {
       mbar_init(do_full(s), 1);
-      mbar_init(do_empty(s), 3);
+      mbar_init(do_empty(s), 1);
       mbar_init(vec_full(s), 64);
     }
     mbar_init(s_full, 1);
@@ -375,6 +571,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tS = tm, tdP = tm + 128, tdV = tm + 256, tdK = tm + 384;
   pdl_wait();
   pdl_launch_dependents();
+  if (warp == 0) {
+    const int4 x = P.whole ? make_int4(0, 0, 0, unit_of(0) < P.num_units) : find_share(P, lane);
+    if (lane == 0) sts4(share, x.x, x.y, x.z, x.w);
+  }
+  __syncthreads();
+  const int4 start = lds_int4(share);
 
   // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
@@ -384,18 +586,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ---------------------------------------------------------- producer
         uint32_t nu = 0, n = 0, nq = 0;   // nq: loads of Q
         bool ok = true;
-        int32_t r = 0;
-        for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-          const KeyUnit x = key_unit(P, u);
-          if (x.ia >= x.ib) continue;
+        Segment x;
+        for (x.begin(P, start); ok && x.left > 0; x.next(P)) {
           if (!wait_asleep(kv_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
           mbar_arrive_expect_tx(kv_full, 2 * TILE_BYTES);
           load_tile(sK, &mapK, kv_full, x.kvh, x.kb * BT, x.shard);
           load_tile(sV, &mapV, kv_full, x.kvh, x.kb * BT, x.shard);
           ++nu;
-          for (int32_t g = 0; ok && g < P.group; ++g) {
-            const int32_t head = x.kvh * P.group + g;
-            for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
+          {
+            int32_t head = x.kvh * P.group + x.s0 / x.ni, i = x.ia + x.s0 % x.ni;
+            for (int32_t st = x.s0; st < x.s1; ++st, ++n) {
               if (!wait_asleep(q_empty(n), ((n / NA) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) {
                 ok = false;
                 break;
@@ -412,6 +612,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 load_tile(sdO(n), &mapdO, do_full(n), head, i * BT, x.shard);
               }
               ++nq;
+              if (++i == x.ia + x.ni) {
+                i = x.ia;
+                ++head;
+              }
             }
           }
         }
@@ -433,11 +637,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         auto wait_do = [&](uint32_t m) {
           return wait_asleep(do_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull);
         };
-        int32_t r = 0;
-        for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-          const KeyUnit x = key_unit(P, u);
-          const int32_t steps = P.group * (x.ib - x.ia);
-          if (x.ia >= x.ib) continue;
+        Segment x;
+        for (x.begin(P, start); ok && x.left > 0; x.next(P)) {
+          const int32_t steps = x.s1 - x.s0;
           if (!wait_asleep(kv_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_q(n)) break;
           tc_fence_after();
           mma_tiles(tS, sK, sQ(n));
@@ -491,21 +693,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
     } else {
       // --------------- per-query numbers of each step, and the look at its rows
-      uint32_t n = 0;
+      uint32_t n = 0, nu = 0;
       bool ok = true;
-      int32_t r = 0;
       const int me = (warp - 2) * 32 + lane;   // 0..63: rows me and me + 64 of the tile
-      for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-        const KeyUnit x = key_unit(P, u);
-        for (int32_t g = 0; ok && g < P.group; ++g) {
-          const int64_t row0 =
-              (static_cast<int64_t>(x.shard) * P.hq + x.kvh * P.group + g) * P.T;
-          for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
+      Segment x;
+      for (x.begin(P, start); ok && x.left > 0; x.next(P), ++nu) {
+        {
+          int32_t g = x.s0 / x.ni, i = x.ia + x.s0 % x.ni;
+          for (int32_t s = x.s0; s < x.s1; ++s, ++n) {
+            const int64_t row0 =
+                (static_cast<int64_t>(x.shard) * P.hq + x.kvh * P.group + g) * P.T;
             const bool cut = !tile_span(P.mask, i, P.tiles, P.T, P.causal).whole(x.kb);
             float lse[2], dl[2];
+            bool only[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int32_t q = i * BT + h * 64 + me;
+              const int2 keys = cut ? row_span(P.mask, q, P.T, P.causal) : make_int2(0, 0);
+              only[h] = keys.y - keys.x == 1;
               const bool in = q < P.T;
               lse[h] = in ? -kLog2e * P.LSE[row0 + q] : -INFINITY;   // P = 0 behind the last row
               dl[h] = in ? -P.delta[row0 + q] : 0.0f;
@@ -518,28 +723,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               sts(vec(n, 0) + (h * 64 + me) * 4, lse[h]);
               sts(vec(n, 1) + (h * 64 + me) * 4, dl[h]);
             }
-            if (me == 0) cut_flag[n % NB] = cut;
-            ok = wait_asleep(q_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull) &&
-                 (!cut || wait_asleep(do_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitFull));
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (cut) {
-#pragma unroll
+            // (vec_full comes before the products that read the tiles, and their
+            // commits before the next loads)
+            const uint32_t odd0 = __ballot_sync(0xffffffffu, cut && !(fabsf(dl[0]) < INFINITY));
+            const uint32_t odd1 = __ballot_sync(0xffffffffu, cut && !(fabsf(dl[1]) < INFINITY));
+            const bool look = (odd0 | odd1) != 0;
+            if (me == 0) {
+              float slope2 = 0.0f;
+              if (BIAS) slope2 = kLog2e * P.slopes[x.shard * P.hq + x.kvh * P.group + g];
+              sts4(about + (n % NB) * 16, i,
+                   (cut ? kCut : 0) | (s == x.s0 ? kFirst : 0) | (s + 1 == x.s1 ? x.last() ? kLast | kEnd : kLast : 0),
+                   __float_as_int(slope2), 0);
+              if (s == x.s0)
+                sts4(about_unit + (nu & 3) * 16, x.kb, x.hh, x.whole() ? -1 : x.s0 > 0 ? 0 : 1, 0);
+            }
+            uint32_t w[2] = {0u, 0u};
+            if (look) {
+              ok = wait_asleep(q_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull) &&
+                   wait_asleep(do_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitFull);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+#pragma unroll 1
               for (int h = 0; h < 2; ++h) {
                 const int row = h * 64 + me;
                 const bool b0 = row_not_finite(sQ(n), row), b1 = row_not_finite(sdO(n), row);
                 if (b0) zero_row(sQ(n), row);
                 if (b1) zero_row(sdO(n), row);
-                const uint32_t w = __ballot_sync(0xffffffffu, b0 || b1);
-                if (lane == 0) bad[(n % NB) * 4 + h * 2 + (warp - 2)] = w;
+                w[h] = __ballot_sync(0xffffffffu, b0 || b1);
               }
               fence_proxy_async_smem();
             }
+            if (cut) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t one = __ballot_sync(0xffffffffu, only[h]);
+                if (lane == 0) {
+                  bad[(n % NB) * 4 + h * 2 + (warp - 2)] = w[h];
+                  lone[(n % NB) * 4 + h * 2 + (warp - 2)] = one;
+                }
+              }
+            }
             mbar_arrive(vec_full(n));
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(q_empty(n));
-              mbar_arrive(do_empty(n));
+            if (++i == x.ia + x.ni) {
+              i = x.ia;
+              ++g;
             }
           }
         }
@@ -553,70 +780,84 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t off = (static_cast<uint32_t>(quad * 32) << 16) + part * 32;
     uint32_t n = 0, nu = 0;
     bool ok = true;
-    int32_t r = 0;
-    for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-      const KeyUnit x = key_unit(P, u);
-      if (x.ia >= x.ib) continue;
-      const int32_t key = x.kb * BT + quad * 32 + lane;
-      const int2 by = key_span(P.mask, key, P.T, P.causal);   // queries that see the key
-      for (int32_t g = 0; ok && g < P.group; ++g) {
-        float slope2 = 0.0f;
-        if (BIAS) slope2 = kLog2e * P.slopes[x.shard * P.hq + x.kvh * P.group + g];
-        for (int32_t i = x.ia; i < x.ib; ++i, ++n) {
-          ok = wait_asleep(vec_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitAttn) &&
-               wait_asleep(s_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          float w[32];
-          uint32_t v[32], pk[16];
-          tmem_ld_32x32b_x32(tS + off, v);
-          const bool cut = cut_flag[n % NB] != 0;
-          const uint32_t vl = vec(n, 0) + part * 128, vd = vec(n, 1) + part * 128;
-          const int32_t q0 = i * BT + part * 32;
-          const float dist0 = static_cast<float>(q0 - key);
-          const int side = i * BT >= x.kb * BT + BT - 1 ? 1 : i * BT + BT - 1 <= x.kb * BT ? -1 : 0;
-          uint32_t seen = 0xffffffffu;   // columns that see this key
-          if (cut) {
-            const int32_t lo = min(max(by.x - q0, 0), 32), hi = min(max(by.y - q0, 0), 32);
-            seen = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
-            if (seen & bad[(n % NB) * 4 + part]) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
-          }
-          auto sees = [&](int e) { return ((seen >> e) & 1u) != 0; };
-          tmem_ld_wait();
-          tc_fence_before();
-          mbar_arrive(s_free);
-          prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut,
-                                [&](int e) { return lds2(vl + e * 4); }, sees);
-          ok = wait_asleep(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          tmem_ld_32x32b_x32(tdP + off, v);
-          tmem_ld_wait();
-          // P^T and dS^T over this quarter's own dP^T
-          tmem_st_32x32b_x16(tdP + off, pk);
-          grad_chunk(v, w, pk, cut, [&](int e) { return lds2(vd + e * 4); }, sees);
-          tmem_st_32x32b_x16(tdP + off + 16, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(ds_full);
-        }
-      }
+    int32_t key = 0;
+    int2 by = make_int2(0, 0);   // queries that see the key
+    for (bool end = start.w == 0; !end; ++n) {
+      ok = wait_asleep(vec_full(n), (n / NB) & 1, abort_flag, P.wait, kErrWaitAttn);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      const int4 step = lds_int4(about + (n % NB) * 16);
+      end = (step.y & kEnd) != 0;
+      if (step.y & kFirst) {
+        key = lds_int4(about_unit + (nu & 3) * 16).x * BT + quad * 32 + lane;
+        by = key_span(P.mask, key, P.T, P.causal);
+      }
+      ok = wait_asleep(s_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      float w[32];
+      uint32_t v[32], pk[16];
+      tmem_ld_32x32b_x32(tS + off, v);
+      const bool cut = (step.y & kCut) != 0;
+      const uint32_t vl = vec(n, 0) + part * 128, vd = vec(n, 1) + part * 128;
+      const int32_t q0 = step.x * BT + part * 32;
+      const float dist0 = static_cast<float>(q0 - key);
+      const int32_t kb = key / BT;
+      const int side = step.x > kb ? 1 : step.x < kb ? -1 : 0;
+      uint32_t seen = 0xffffffffu;   // columns that see this key
+      if (cut) {
+        const int32_t lo = min(max(by.x - q0, 0), 32), hi = min(max(by.y - q0, 0), 32);
+        seen = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+        if (seen & bad[(n % NB) * 4 + part]) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
+      }
+      auto sees = [&](int e) { return ((seen >> e) & 1u) != 0; };
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(s_free);
+      prob_chunk<CAP, BIAS>(v, w, pk, P, __int_as_float(step.z), dist0, side, cut,
+                            [&](int e, uint64_t& a, uint64_t& b) { lds4(vl + e * 4, a, b); }, sees);
+      const uint32_t one = cut ? lone[(n % NB) * 4 + part] : 0u;
+      if (one != 0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if ((one >> e) & 1u) w[e] *= 0.0f;
+      }
+      ok = wait_asleep(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld_32x32b_x32(tdP + off, v);
+      tmem_ld_wait();
+      // P^T and dS^T over this quarter's own dP^T
+      tmem_st_32x32b_x16(tdP + off, pk);
+      grad_chunk(v, w, pk, cut, [&](int e, uint64_t& a, uint64_t& b) { lds4(vd + e * 4, a, b); }, sees);
+      tmem_st_32x32b_x16(tdP + off + 16, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+      if (!(step.y & kLast)) continue;
       ok = wait_asleep(acc_full, nu & 1, abort_flag, P.wait, kErrWaitAttn);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       // keys of no document stay as they were
       const bool store = key < P.T && by.y >= 0;
-      const int64_t row =
-          ((static_cast<int64_t>(x.shard) * P.T + key) * P.hkv + x.kvh) * DH + part * 32;
+      const int4 unit = lds_int4(about_unit + (nu & 3) * 16);
+      const int32_t shard = unit.y / P.hkv, kvh = unit.y - shard * P.hkv;
+      const int64_t row = ((static_cast<int64_t>(shard) * P.T + key) * P.hkv + kvh) * DH + part * 32;
       const uint32_t hits = *const_cast<volatile uint32_t*>(&hit[(nu % 3) * 4 + quad]);
       const float f = (hits >> lane) & 1u ? NAN : 1.0f;
       if (part == 0 && lane == 0) hit[((nu + 2) % 3) * 4 + quad] = 0;
-      store_part_row(tdV + off, f, store, P.dV + row);
-      store_part_row(tdK + off, f * P.s.scale, store, P.dK + row);
+      if (unit.z < 0) {
+        store_part_row(tdV + off, f, store, P.dV + row);
+        store_part_row(tdK + off, f * P.s.scale, store, P.dK + row);
+      } else {
+        float* const to = P.part + (static_cast<int64_t>(blockIdx.x) * 2 + unit.z) * PART_FLOATS +
+                          (quad * 32 + lane) * DH + part * 32;
+        keep_part_row(tdV + off, f, to);
+        keep_part_row(tdK + off, f * P.s.scale, to + BT * DH);
+      }
       tc_fence_before();
       mbar_arrive(acc_empty);
       ++nu;
@@ -627,6 +868,53 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
+  }
+}
+
+// Adds the parts of the unit that the beginning of CTA c = blockIdx.x + 1's
+// share cuts (the first such CTA's block does it), in the CTAs' order; 16 keys a
+// block.
+constexpr int JOIN_KEYS = 16;
+__global__ void __launch_bounds__(256) dkv_join_kernel(const __grid_constant__ BwdParams P, int32_t ctas) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t c = blockIdx.x + 1;
+  const int64_t total = *P.total;
+  const int64_t w = share_of(total, c, ctas);
+  if (w >= share_of(total, c + 1, ctas)) return;   // (fewer steps than CTAs)
+  const int4 cut = P.cuts[c];
+  const int64_t from = w - cut.z, to = from + cut.w;   // the unit's steps on the line
+  int64_t first = c - 1;   // the CTA before with a share
+  while (first > 0 && share_of(total, first, ctas) == w) --first;
+  if (cut.z == 0 || share_of(total, first, ctas) > from) return;
+  const int32_t row0 = blockIdx.y * JOIN_KEYS;
+  constexpr int VECS = JOIN_KEYS * DH / 4 / 256;   // float4s of a thread in each of dV, dK
+  float4 sum[2][VECS];
+  auto add = [&](int64_t cta, int slot, bool first) {
+    const float* part = P.part + (cta * 2 + slot) * PART_FLOATS + row0 * DH;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(part + a * BT * DH + (threadIdx.x + i * 256) * 4);
+        float4& t = sum[a][i];
+        t = first ? x : make_float4(t.x + x.x, t.y + x.y, t.z + x.z, t.w + x.w);
+      }
+    }
+  };
+  add(first, 1, true);
+  for (int64_t d = c; d < ctas && share_of(total, d, ctas) < to; ++d)
+    if (share_of(total, d, ctas) < share_of(total, d + 1, ctas)) add(d, 0, false);
+  const int32_t shard = cut.y / P.hkv, kvh = cut.y - shard * P.hkv;
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int32_t at = (threadIdx.x + i * 256) * 4, key = cut.x * BT + row0 + at / DH;
+    if (key >= P.T || key_span(P.mask, key, P.T, P.causal).y < 0) continue;
+    const int64_t out = ((static_cast<int64_t>(shard) * P.T + key) * P.hkv + kvh) * DH + at % DH;
+    *reinterpret_cast<uint2*>(P.dV + out) =
+        make_uint2(pack2(sum[0][i].x, sum[0][i].y), pack2(sum[0][i].z, sum[0][i].w));
+    *reinterpret_cast<uint2*>(P.dK + out) =
+        make_uint2(pack2(sum[1][i].x, sum[1][i].y), pack2(sum[1][i].z, sum[1][i].w));
   }
 }
 
@@ -686,7 +974,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(qd_empty, 1);
     for (int s = 0; s < NA; ++s) {
       mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 3);   // the MMA thread's commit, warps 2 and 3
+      mbar_init(k_empty(s), 1);
       mbar_init(k_seen(s), 64);
     }
     for (int s = 0; s < NB; ++s) {
@@ -837,21 +1125,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
         const QueryUnit x = query_unit(P, u);
         for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
+          const bool cut = !x.t.whole(j);
+          bool odd = false;
+          if (cut) {
+            const uint8_t* flags = P.k_bad + (static_cast<int64_t>(x.shard) * P.hkv + x.kvh) * P.T;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int32_t key = j * BT + h * 64 + (warp - 2) * 32 + lane;
+              odd |= key < P.T && flags[key] != 0;
+            }
+          }
           ok = wait_asleep(k_full(n), (n / NA) & 1, abort_flag, P.wait, kErrWaitFull);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (!x.t.whole(j)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int row = h * 64 + (warp - 2) * 32 + lane;
-              if (row_not_finite(sK(n), row)) zero_row(sK(n), row);
+          if (cut) {
+            if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                const int row = h * 64 + (warp - 2) * 32 + lane;
+                if (row_not_finite(sK(n), row)) zero_row(sK(n), row);
+              }
+              fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
             mbar_arrive(k_seen(looked));
             ++looked;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(k_empty(n));
         }
       }
     }
@@ -896,7 +1194,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_ld_32x32b_x32(tS, v);
         tmem_ld_wait();
         // (P itself is not stored: dQ needs dS alone)
-        prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut, [&](int) { return nlse; }, sees);
+        prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut, [&](int, uint64_t& a, uint64_t& b) { a = b = nlse; }, sees);
+        if (cut && span.y - span.x == 1) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] *= 0.0f;
+        }
         ok = wait_asleep(dp_full, n & 1, abort_flag, P.wait, kErrWaitAttn);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -905,7 +1207,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(dp_free);
-        grad_chunk(v, w, pk, cut, [&](int) { return ndl; }, sees);
+        grad_chunk(v, w, pk, cut, [&](int, uint64_t& a, uint64_t& b) { a = b = ndl; }, sees);
         tmem_st_32x32b_x16(tS, pk);
         tmem_st_wait();
         tc_fence_before();
@@ -953,10 +1255,16 @@ tp_status launch_bwd(const LaunchCtx& c, BwdParams prm, const ScoreCall& a, cons
     }
   }
   auto grid = [&](int32_t units) { return dim3(units < c.num_sms ? units : c.num_sms); };
+  const int32_t ctas = static_cast<int32_t>(score_dkv_ctas(a));
   prm.num_units = prm.p * prm.hkv * prm.tiles;
-  cudaError_t e = launch_pdl(tc_scored_dkv_kernel<CAP, BIAS>, grid(prm.num_units), dim3(NUM_THREADS),
+  prm.whole = prm.mask.rows == nullptr && prm.num_units >= kWholeUnits * ctas;
+  cudaError_t e = launch_pdl(tc_scored_dkv_kernel<CAP, BIAS>, dim3(ctas), dim3(NUM_THREADS),
                              SMEM_BYTES, c.stream, mQ, mK, mV, mdO, prm);
   note_launch();
+  if (e == cudaSuccess && ctas > 1 && !prm.whole) {
+    e = launch_pdl(dkv_join_kernel, dim3(ctas - 1, BT / JOIN_KEYS), dim3(256), 0, c.stream, prm, ctas);
+    note_launch();
+  }
   if (e == cudaSuccess) {
     prm.debug_drop = -1;   // an armed fault injection applies to the first launch only
     prm.num_units = prm.p * prm.hq * prm.tiles;
@@ -973,19 +1281,33 @@ tp_status launch_bwd(const LaunchCtx& c, BwdParams prm, const ScoreCall& a, cons
 
 }  // namespace
 
+// CTAs that share the steps of dK and dV: one an SM, fewer where they would get
+// less than two steps each even without a mask.
+int64_t score_dkv_ctas(const ScoreCall& a) {
+  const int64_t tiles = ceil_div(a.T, BT);
+  const int64_t steps = static_cast<int64_t>(a.p) * a.hq * (a.causal ? tiles * (tiles + 1) / 2 : tiles * tiles);
+  const int64_t most = (steps + 1) / 2;
+  return most < kScoreDkvCtas ? (most < 1 ? 1 : most) : kScoreDkvCtas;
+}
+size_t score_dkv_bytes(const ScoreCall& a) {
+  return static_cast<size_t>(score_dkv_ctas(a)) * (2 * PART_FLOATS * sizeof(float) + sizeof(int4)) + 256;
+}
+
 tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a) {
   CUtensorMap mQ, mK, mV, mdO;
   const int64_t wq = static_cast<int64_t>(a.hq) * DH, wk = static_cast<int64_t>(a.hkv) * DH;
   if (!make_map_a(&mQ, a.Q, wq, a.T, a.p) || !make_map_a(&mK, a.K, wk, a.T, a.p) ||
       !make_map_a(&mV, a.V, wk, a.T, a.p) || !make_map_a(&mdO, a.dO, wq, a.T, a.p))
     return TP_ERR_CUDA;
-  const int64_t rows = a.T * a.p * a.hq;
-  const cudaError_t e =
-      launch_pdl(score_delta_kernel, dim3(static_cast<unsigned>((rows + DELTA_ROWS - 1) / DELTA_ROWS)),
-                 dim3(256), 0,
-                 c.stream, static_cast<const __nv_bfloat16*>(a.O),
-                 static_cast<const __nv_bfloat16*>(a.dO), a.delta, rows, static_cast<int32_t>(a.T),
-                 static_cast<int32_t>(a.hq));
+  const int64_t shard_rows = static_cast<int64_t>(a.p) * a.T;
+  const int64_t q_blocks = (shard_rows * a.hq + DELTA_ROWS - 1) / DELTA_ROWS;
+  const int64_t k_blocks = (shard_rows * a.hkv + DELTA_ROWS - 1) / DELTA_ROWS;
+  cudaError_t e = launch_pdl(
+      score_delta_kernel, dim3(static_cast<unsigned>(q_blocks + k_blocks)), dim3(256), 0, c.stream,
+      static_cast<const __nv_bfloat16*>(a.O), static_cast<const __nv_bfloat16*>(a.dO),
+      static_cast<const __nv_bfloat16*>(a.Q), static_cast<const __nv_bfloat16*>(a.K), a.delta, a.k_bad,
+      static_cast<uint32_t>(q_blocks), shard_rows, static_cast<int32_t>(a.T),
+      static_cast<int32_t>(a.hq), static_cast<int32_t>(a.hkv));
   note_launch();
   if (e != cudaSuccess) {
     set_error_detail("delta launch failed: %s", cudaGetErrorString(e));
@@ -1005,6 +1327,10 @@ tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a) {
   prm.slopes = a.slopes;
   prm.LSE = a.LSE;
   prm.delta = a.delta;
+  prm.k_bad = a.k_bad;
+  prm.part = a.part;
+  prm.cuts = reinterpret_cast<int4*>(a.part + score_dkv_ctas(a) * 2 * PART_FLOATS);
+  prm.total = reinterpret_cast<int64_t*>(prm.cuts + score_dkv_ctas(a));
   prm.dQ = static_cast<__nv_bfloat16*>(a.dQ);
   prm.dK = static_cast<__nv_bfloat16*>(a.dK);
   prm.dV = static_cast<__nv_bfloat16*>(a.dV);

@@ -368,12 +368,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                           kErrWaitAttn)))
             break;
           tc_fence_after();
-          const uint32_t k = sK(w.n), d = tmem_base + (w.n % NS) * BKV;
+          const uint32_t q = desc_lo(sQ, 16), k = desc_lo(sK(w.n), 16);
+          const uint32_t d = tmem_base + (w.n % NS) * BKV;
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-            tc_mma_f16(d, smem_desc_sw128(sQ + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024),
-                       IDESC_S, kk > 0 ? 1u : 0u);
+            const uint32_t off = desc_step((kk >> 2) * HALF_BYTES + (kk & 3) * 32);
+            tc_mma_f16_lo(d, q + off, k + off, IDESC_S, kk > 0 ? 1u : 0u);
           }
           tc_commit(s_full(w.n));
           tc_commit(k_empty(w.n));
@@ -393,12 +393,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               !wait_asleep(p_full(w.n), (w.n / NS) & 1, abort_flag, P.wait, kErrWaitAttn))
             break;
           tc_fence_after();
-          const uint32_t v = sV(w.n), pa = tmem_base + (w.n % NS) * BKV;
+          const uint32_t v = desc_lo(sV(w.n), HALF_BYTES), pa = tmem_base + (w.n % NS) * BKV;
 #pragma unroll
           for (int kk = 0; kk < BKV / 16; ++kk)
-            tc_mma_f16_ts(tmem_base + O_COL0, pa + (kk >> 2) * 64 + (kk & 3) * 8,
-                          smem_desc_sw128(v + kk * 16 * 128, HALF_BYTES, 1024), IDESC_O,
-                          (!w.first || kk > 0) ? 1u : 0u);
+            tc_mma_f16_ts_lo(tmem_base + O_COL0, pa + (kk >> 2) * 64 + (kk & 3) * 8,
+                             v + desc_step(kk * 16 * 128), IDESC_O, (!w.first || kk > 0) ? 1u : 0u);
           tc_commit(pv_done(w.n));
           tc_commit(v_empty(w.n));
           if (w.last()) tc_commit(o_full);

@@ -78,6 +78,8 @@ struct ScoreCall {
   const void* dO;          // backward
   void *dQ, *dK, *dV;
   float* delta;            // backward: [p][hq][T] scratch
+  uint8_t* k_bad;          // backward: [p][hkv][T] scratch
+  float* part;             // backward: score_dkv_bytes() of scratch
   int64_t T;
   int p, hq, hkv;          // heads per shard
   bool causal;
@@ -104,6 +106,11 @@ tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a);
 
 cudaError_t launch_attention_mask(const LaunchCtx& c, const int32_t* off, int n_docs,
                                   const int32_t* prefix, bool causal, void* mask, int64_t T);
+// Scratch of the backward's dK and dV for the call's sizes; kScoreDkvCtas: the
+// SMs of a B200.
+constexpr int kScoreDkvCtas = 148;
+int64_t score_dkv_ctas(const ScoreCall& a);
+size_t score_dkv_bytes(const ScoreCall& a);
 tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a);
 tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a);
 

@@ -221,3 +221,37 @@ def test_a_dropped_load_times_out(launch):
         tp.tp_set_wait_timeout_ns(0)
         tp.tp_debug_drop_load(-1)
     _check(case, host, slopes, seen, inside, O, LSE, _call(case, dev, score, O, LSE))
+
+
+@pytest.mark.parametrize("case,heads", [
+    # 900 key tiles: each CTA takes several whole ones in turn
+    (dict(p=1, T=129, h=450, hkv=450, cap=30.0), [(0, 0), (0, 222), (0, 449)]),
+    # as many behind a mask, whose empty and short tiles lie on the CTAs' shares
+    (dict(p=2, T=270, h=300, hkv=300, off=[3, 4, 130, 131, 260], slopes=1.0), [(0, 0), (0, 77), (1, 149)]),
+    # shares of a few steps, each tile's sums on many CTAs
+    (dict(p=1, T=600, h=24, hkv=1, slopes=1.0), [(0, 0)]),
+], ids=["whole", "mask", "split"])
+def test_key_tiles_dealt_to_the_ctas(case, heads):
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    grads = _call(case, dev, score, O, LSE)
+    _check(case, host, slopes, seen, inside, O, LSE, grads, kv_heads=heads)
+    assert all(torch.equal(a, b) for a, b in zip(grads, _call(case, dev, score, O, LSE)))
+
+
+@pytest.mark.parametrize("case", [
+    dict(p=2, T=1, h=4, hkv=2, slopes=1.0),
+    dict(p=1, T=200, h=2, hkv=1, off=list(range(3, 198)), cap=30.0),
+    dict(p=1, T=140, h=2, hkv=2, off=[0, 1, 2, 3, 140], causal=False),
+], ids=["token", "documents", "some"])
+def test_a_query_with_one_key_has_no_gradient(case):
+    # softmax of one score is 1 whatever the score: exact zeros, not the rounding of dP - D
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    dQ, dK, dV = _call(case, dev, score, O, LSE)
+    one = torch.from_numpy(seen.sum(1) == 1).cuda() & torch.from_numpy(inside).cuda()
+    assert one.any() and torch.all(dQ[:, one] == 0)
+    alone = one & torch.from_numpy(seen.sum(0) == 1).cuda()
+    assert torch.all(dK[:, alone] == 0)
+    # an infinite key is still seen
+    dev[1][:, one.nonzero()[0, 0]] = float("nan")
+    dQ, dK, dV = _call(case, dev, score, O, LSE)
+    assert torch.all(torch.isnan(dQ[:, one.nonzero()[0, 0]]))
