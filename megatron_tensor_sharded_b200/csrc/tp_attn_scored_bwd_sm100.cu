@@ -627,67 +627,74 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
+      {
         // -------------------------------------------------------- MMA issuer
+        // The whole warp goes through the loop and one lane issues: what the
+        // products' operands are made of is then the same for the warp, and
+        // stays in uniform registers.
+        const bool leader = elect_one();
+        auto await = [&](uint32_t bar, uint32_t parity, unsigned code) {
+          return __all_sync(0xffffffffu, wait_asleep(bar, parity, abort_flag, P.wait, code)) != 0;
+        };
         uint32_t n = 0, nu = 0;
         bool ok = true;
         auto wait_q = [&](uint32_t m) {
-          return wait_asleep(q_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull);
+          return await(q_full(m), (m / NA) & 1, kErrWaitFull);
         };
         auto wait_do = [&](uint32_t m) {
-          return wait_asleep(do_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull);
+          return await(do_full(m), (m / NB) & 1, kErrWaitFull);
         };
         Segment x;
         for (x.begin(P, start); ok && x.left > 0; x.next(P)) {
           const int32_t steps = x.s1 - x.s0;
-          if (!wait_asleep(kv_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !wait_q(n)) break;
+          if (!await(kv_full, nu & 1, kErrWaitFull) || !wait_q(n)) break;
           tc_fence_after();
-          mma_tiles(tS, sK, sQ(n));
-          tc_commit(s_full);
+          if (leader) mma_tiles(tS, sK, sQ(n));
+          if (leader) tc_commit(s_full);
           if (!wait_do(n)) break;
           tc_fence_after();
-          mma_tiles(tdP, sV, sdO(n));
-          tc_commit(dp_full);
-          if (steps == 1) tc_commit(kv_empty);
+          if (leader) mma_tiles(tdP, sV, sdO(n));
+          if (leader) tc_commit(dp_full);
+          if (leader && steps == 1) tc_commit(kv_empty);
           for (int32_t s = 0; s < steps; ++s, ++n) {
             const bool more = s + 1 < steps;
             if (more) {
               // the next scores as soon as the warps hold this step's
-              if (!wait_asleep(s_free, n & 1, abort_flag, P.wait, kErrWaitAttn) || !wait_q(n + 1)) {
+              if (!await(s_free, n & 1, kErrWaitAttn) || !wait_q(n + 1)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              mma_tiles(tS, sK, sQ(n + 1));
-              tc_commit(s_full);
+              if (leader) mma_tiles(tS, sK, sQ(n + 1));
+              if (leader) tc_commit(s_full);
             }
-            if (!wait_asleep(ds_full, n & 1, abort_flag, P.wait, kErrWaitAttn) ||
+            if (!await(ds_full, n & 1, kErrWaitAttn) ||
                 (s == 0 && nu > 0 &&
-                 !wait_asleep(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
+                 !await(acc_empty, (nu - 1) & 1, kErrWaitAttn))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            mma_rows(tdV, tdP, sdO(n), s > 0);
-            tc_commit(do_empty(n));
-            mma_rows(tdK, tdP + 16, sQ(n), s > 0);
-            tc_commit(q_empty(n));
+            if (leader) mma_rows(tdV, tdP, sdO(n), s > 0);
+            if (leader) tc_commit(do_empty(n));
+            if (leader) mma_rows(tdK, tdP + 16, sQ(n), s > 0);
+            if (leader) tc_commit(q_empty(n));
             if (more) {
               if (!wait_do(n + 1)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              mma_tiles(tdP, sV, sdO(n + 1));
-              tc_commit(dp_full);
-              if (s + 2 == steps) tc_commit(kv_empty);   // K and V are read by S^T and dP^T alone
+              if (leader) mma_tiles(tdP, sV, sdO(n + 1));
+              if (leader) tc_commit(dp_full);
+              if (leader && s + 2 == steps) tc_commit(kv_empty);   // K and V are read by S^T and dP^T alone
             }
           }
           if (!ok) break;
-          tc_commit(acc_full);
+          if (leader) tc_commit(acc_full);
           ++nu;
         }
-        tc_commit(drain);
+        if (leader) tc_commit(drain);
         wait_teardown(drain, 0, P.wait);
       }
       __syncwarp();
@@ -1053,23 +1060,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
+      {
         // -------------------------------------------------------- MMA issuer
+        // The whole warp goes through the loop and one lane issues: what the
+        // products' operands are made of is then the same for the warp, and
+        // stays in uniform registers.
+        const bool leader = elect_one();
+        auto await = [&](uint32_t bar, uint32_t parity, unsigned code) {
+          return __all_sync(0xffffffffu, wait_asleep(bar, parity, abort_flag, P.wait, code)) != 0;
+        };
         uint32_t n = 0, nu = 0;
         bool ok = true;
         auto issue_s = [&](uint32_t m) {
-          if (!wait_asleep(k_full(m), (m / NA) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
+          if (!await(k_full(m), (m / NA) & 1, kErrWaitFull)) return false;
           tc_fence_after();
-          mma_tiles(tm + (m & 1) * 128, sQ, sK(m));
-          tc_commit(s_full(m & 1));
+          if (leader) mma_tiles(tm + (m & 1) * 128, sQ, sK(m));
+          if (leader) tc_commit(s_full(m & 1));
           return true;
         };
         auto issue_dp = [&](uint32_t m) {
-          if (!wait_asleep(v_full(m), (m / NB) & 1, abort_flag, P.wait, kErrWaitFull)) return false;
+          if (!await(v_full(m), (m / NB) & 1, kErrWaitFull)) return false;
           tc_fence_after();
-          mma_tiles(tdP, sdO, sV(m));
-          tc_commit(v_empty(m));
-          tc_commit(dp_full);
+          if (leader) mma_tiles(tdP, sdO, sV(m));
+          if (leader) tc_commit(v_empty(m));
+          if (leader) tc_commit(dp_full);
           return true;
         };
         int32_t r = 0;
@@ -1077,43 +1091,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const QueryUnit x = query_unit(P, u);
           const int32_t steps = x.t.je - x.t.jb;
           if (steps <= 0) continue;
-          if (!wait_asleep(qd_full, nu & 1, abort_flag, P.wait, kErrWaitFull) || !issue_s(n) ||
+          if (!await(qd_full, nu & 1, kErrWaitFull) || !issue_s(n) ||
               !issue_dp(n))
             break;
-          if (steps == 1)
-            tc_commit(qd_empty);
-          else if (!issue_s(n + 1))
+          if (steps == 1) {
+            if (leader) tc_commit(qd_empty);
+          } else if (!issue_s(n + 1)) {
             break;
+          }
           for (int32_t s = 0; s < steps; ++s, ++n) {
             if (s + 1 < steps) {
               // the warps have read dP of this step
-              ok = wait_asleep(dp_free, n & 1, abort_flag, P.wait, kErrWaitAttn);
+              ok = await(dp_free, n & 1, kErrWaitAttn);
               if (ok) {
                 tc_fence_after();
                 ok = issue_dp(n + 1);
               }
               if (!ok) break;
-              if (s + 2 == steps) tc_commit(qd_empty);
+              if (leader && s + 2 == steps) tc_commit(qd_empty);
             }
-            if (!wait_asleep(ds_full(n), (n >> 1) & 1, abort_flag, P.wait, kErrWaitAttn) ||
+            if (!await(ds_full(n), (n >> 1) & 1, kErrWaitAttn) ||
                 (s == 0 && nu > 0 &&
-                 !wait_asleep(acc_empty, (nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn))) {
+                 !await(acc_empty, (nu - 1) & 1, kErrWaitAttn))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            mma_rows(tdQ, tm + (n & 1) * 128, sK(n), s > 0);
-            tc_commit(k_empty(n));
+            if (leader) mma_rows(tdQ, tm + (n & 1) * 128, sK(n), s > 0);
+            if (leader) tc_commit(k_empty(n));
             if (s + 2 < steps && !issue_s(n + 2)) {
               ok = false;
               break;
             }
           }
           if (!ok) break;
-          tc_commit(acc_full);
+          if (leader) tc_commit(acc_full);
           ++nu;
         }
-        tc_commit(drain);
+        if (leader) tc_commit(drain);
         wait_teardown(drain, 0, P.wait);
       }
       __syncwarp();

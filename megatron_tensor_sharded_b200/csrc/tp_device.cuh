@@ -157,6 +157,17 @@ __device__ __forceinline__ bool wait_teardown(uint32_t bar, uint32_t parity, con
   }
 }
 
+// True in one lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
 // ------------------------------------------------ counters between CTAs (global)
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
   int v;
