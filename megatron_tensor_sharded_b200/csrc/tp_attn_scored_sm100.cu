@@ -358,51 +358,62 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
+      {
         // --------------------------------------------------- S = Q K^T issuer
+        // The whole warp goes through the loop and one lane issues: what the
+        // products' operands are made of is then the same for the warp, and
+        // stays in uniform registers.
+        const bool leader = elect_one();
+        auto await = [&](uint32_t bar, uint32_t parity, unsigned code) {
+          return __all_sync(0xffffffffu, wait_asleep(bar, parity, abort_flag, P.wait, code)) != 0;
+        };
         for (w.begin(P); !w.done; w.next(P)) {
-          if ((w.first && !wait_asleep(q_full, w.nu & 1, abort_flag, P.wait, kErrWaitFull)) ||
-              !wait_asleep(k_full(w.n), (w.n / NK) & 1, abort_flag, P.wait, kErrWaitFull) ||
+          if ((w.first && !await(q_full, w.nu & 1, kErrWaitFull)) ||
+              !await(k_full(w.n), (w.n / NK) & 1, kErrWaitFull) ||
               // the buffer's last probabilities have been used
-              (w.n >= NS && !wait_asleep(pv_done(w.n - NS), ((w.n - NS) / NS) & 1, abort_flag, P.wait,
-                                          kErrWaitAttn)))
+              (w.n >= NS && !await(pv_done(w.n - NS), ((w.n - NS) / NS) & 1, kErrWaitAttn)))
             break;
           tc_fence_after();
           const uint32_t q = desc_lo(sQ, 16), k = desc_lo(sK(w.n), 16);
           const uint32_t d = tmem_base + (w.n % NS) * BKV;
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
+          for (int kk = 0; leader && kk < DH / 16; ++kk) {
             const uint32_t off = desc_step((kk >> 2) * HALF_BYTES + (kk & 3) * 32);
             tc_mma_f16_lo(d, q + off, k + off, IDESC_S, kk > 0 ? 1u : 0u);
           }
-          tc_commit(s_full(w.n));
-          tc_commit(k_empty(w.n));
-          if (w.last()) tc_commit(q_empty);
+          if (leader) tc_commit(s_full(w.n));
+          if (leader) tc_commit(k_empty(w.n));
+          if (leader && w.last()) tc_commit(q_empty);
         }
-        tc_commit(drain);
+        if (leader) tc_commit(drain);
         wait_teardown(drain, 0, P.wait);
       }
       __syncwarp();
     } else if (warp == 3) {
-      if (lane == 0) {
+      {
         // ------------------------------------------------- O += P V issuer
+        // (the same way)
+        const bool leader = elect_one();
+        auto await = [&](uint32_t bar, uint32_t parity, unsigned code) {
+          return __all_sync(0xffffffffu, wait_asleep(bar, parity, abort_flag, P.wait, code)) != 0;
+        };
         for (w.begin(P); !w.done; w.next(P)) {
           if ((w.first && w.nu > 0 &&
-               !wait_asleep(o_empty, (w.nu - 1) & 1, abort_flag, P.wait, kErrWaitAttn)) ||
-              !wait_asleep(v_seen(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull) ||
-              !wait_asleep(p_full(w.n), (w.n / NS) & 1, abort_flag, P.wait, kErrWaitAttn))
+               !await(o_empty, (w.nu - 1) & 1, kErrWaitAttn)) ||
+              !await(v_seen(w.n), (w.n / NV) & 1, kErrWaitFull) ||
+              !await(p_full(w.n), (w.n / NS) & 1, kErrWaitAttn))
             break;
           tc_fence_after();
           const uint32_t v = desc_lo(sV(w.n), HALF_BYTES), pa = tmem_base + (w.n % NS) * BKV;
 #pragma unroll
-          for (int kk = 0; kk < BKV / 16; ++kk)
+          for (int kk = 0; leader && kk < BKV / 16; ++kk)
             tc_mma_f16_ts_lo(tmem_base + O_COL0, pa + (kk >> 2) * 64 + (kk & 3) * 8,
                              v + desc_step(kk * 16 * 128), IDESC_O, (!w.first || kk > 0) ? 1u : 0u);
-          tc_commit(pv_done(w.n));
-          tc_commit(v_empty(w.n));
-          if (w.last()) tc_commit(o_full);
+          if (leader) tc_commit(pv_done(w.n));
+          if (leader) tc_commit(v_empty(w.n));
+          if (leader && w.last()) tc_commit(o_full);
         }
-        tc_commit(drain + 8);
+        if (leader) tc_commit(drain + 8);
         wait_teardown(drain + 8, 0, P.wait);
       }
       __syncwarp();
