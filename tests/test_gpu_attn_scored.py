@@ -193,3 +193,16 @@ def test_a_dropped_load_times_out():
         tp.tp_debug_drop_load(-1)
     tp.tp_attention_scored(Q, Q, Q, O, None, T, 1, 1, 1, 128, tp.score_params(causal=True))
     tp.tp_sync_status()
+
+
+@pytest.mark.parametrize("case", [dict(p=1, T=300, h=2, hkv=1, off=[0, 100, 290], cap=30.0),
+                                  dict(p=1, T=270, h=2, hkv=2, off=[5, 140, 261], slopes=1.0)], ids=["cap", "bias"])
+def test_large_values_are_not_taken_for_infinities(case):
+    # a factor of 2^90 in V is the same factor in O, bit for bit: products of
+    # two such values are beyond bf16 and fp32
+    def enlarge(Q, K, V, inside):
+        V *= 2.0 ** 90
+
+    inside, O = _run(case)[3:5]
+    large = _run(case, poison=enlarge)[4]
+    assert np.array_equal(large[:, inside], O[:, inside] * 2.0 ** 90)
