@@ -68,6 +68,7 @@ constexpr int VEC_BYTES = 2 * BT * 4;        // per slot: -LSE log2 e, -D
 // 224 KB of tiles: no room to round the start up, it has to be aligned (checked)
 constexpr int TILES_BYTES = (2 + NA + NB) * TILE_BYTES;
 constexpr int SMEM_BYTES = TILES_BYTES + NB * VEC_BYTES + 512;
+static_assert(2 * kOrderTiles * 2 <= NB * VEC_BYTES, "dq keeps its order of tiles in place of the vectors");
 constexpr int NUM_THREADS = 640;
 constexpr int ARITH = 512;                   // threads that form P and dS
 constexpr uint32_t IDESC_KK = idesc_bf16_f32(BT, BT, 0, 0);   // both operands along head_dim
@@ -930,10 +931,10 @@ struct QueryUnit {
   int32_t shard, head, kvh, qb;
   TileSpan t;
 };
-__device__ __forceinline__ QueryUnit query_unit(const BwdParams& P, int32_t u) {
+__device__ __forceinline__ QueryUnit query_unit(const BwdParams& P, int32_t u, const uint16_t* order) {
   QueryUnit x;
   const int32_t heads = P.p * P.hq, hh = u % heads;
-  x.qb = P.tiles - 1 - u / heads;   // causal: the longest first
+  x.qb = order != nullptr ? order[u / heads] : P.tiles - 1 - u / heads;   // causal: the longest first
   x.shard = hh / P.hq;
   x.head = hh % P.hq;
   x.kvh = x.head / P.group;
@@ -1017,6 +1018,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tdP = tm + 256, tdQ = tm + 384;   // S buffers at 0 and 128
   pdl_wait();
   pdl_launch_dependents();
+  uint16_t* const order_smem = reinterpret_cast<uint16_t*>(ctrl + 512);
+  const uint16_t* const order =
+      order_tiles(P.mask, P.tiles, P.T, P.causal, P.num_units <= static_cast<int32_t>(gridDim.x),
+                  order_smem, order_smem + kOrderTiles);
 
   // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
@@ -1028,7 +1033,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         bool ok = true;
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-          const QueryUnit x = query_unit(P, u);
+          const QueryUnit x = query_unit(P, u, order);
           if (x.t.jb >= x.t.je) continue;
           if (!wait_asleep(qd_empty, (nu & 1) ^ 1u, abort_flag, P.wait, kErrWaitAttn)) break;
           mbar_arrive_expect_tx(qd_full, 2 * TILE_BYTES);
@@ -1088,7 +1093,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
         int32_t r = 0;
         for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-          const QueryUnit x = query_unit(P, u);
+          const QueryUnit x = query_unit(P, u, order);
           const int32_t steps = x.t.je - x.t.jb;
           if (steps <= 0) continue;
           if (!await(qd_full, nu & 1, kErrWaitFull) || !issue_s(n) ||
@@ -1138,7 +1143,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       int32_t r = 0;
       for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-        const QueryUnit x = query_unit(P, u);
+        const QueryUnit x = query_unit(P, u, order);
         for (int32_t j = x.t.jb; j < x.t.je; ++j, ++n) {
           const bool cut = !x.t.whole(j);
           bool odd = false;
@@ -1178,7 +1183,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     int32_t r = 0;
     for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-      const QueryUnit x = query_unit(P, u);
+      const QueryUnit x = query_unit(P, u, order);
       if (x.t.jb >= x.t.je) continue;
       const int32_t q0 = x.qb * BT, q = q0 + quad * 32 + lane;
       const int2 span = row_span(P.mask, q, P.T, P.causal);

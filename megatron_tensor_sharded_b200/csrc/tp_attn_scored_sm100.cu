@@ -83,7 +83,7 @@ constexpr int TILES_BYTES = (1 + NK + NV) * TILE_BYTES;
 // floats: [group][half][row] maxima, [group][row] running maximum, and
 // [unit parity][sum, maximum, mark][part][row] for the unit's end
 constexpr int XCH_FLOATS = 2 * 2 * BQ + 2 * BQ + 2 * 3 * 4 * BQ;
-constexpr int SMEM_BYTES = 1024 + TILES_BYTES + XCH_FLOATS * 4 + 512;
+constexpr int SMEM_BYTES = 1024 + TILES_BYTES + XCH_FLOATS * 4 + 512 + 2 * kOrderTiles * 2;
 constexpr int NUM_THREADS = 640;
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BQ, BKV, 0, 0);
 constexpr uint32_t IDESC_O = idesc_bf16_f32(BQ, DH, 0, 1);
@@ -109,11 +109,11 @@ struct Unit {
   TileSpan t;
 };
 
-__device__ __forceinline__ Unit decode_unit(const ScoredParams& P, int32_t u) {
+__device__ __forceinline__ Unit decode_unit(const ScoredParams& P, int32_t u, const uint16_t* order) {
   Unit x;
   const int32_t heads = P.p * P.hq;
   const int32_t level = u / heads, hh = u - level * heads;
-  x.qb = P.q_blocks - 1 - level;   // causal: the longest first
+  x.qb = order != nullptr ? order[level] : P.q_blocks - 1 - level;   // causal: the longest first
   x.shard = hh / P.hq;
   x.head = hh - x.shard * P.hq;
   x.kvh = x.head / P.group;
@@ -139,9 +139,10 @@ struct Walk {
   int32_t r, u, j;   // round, unit, block
   uint32_t n, nu;    // blocks and units before this one
   bool first, done;  // the unit's first block; the walk is over
+  const uint16_t* order;
   __device__ __forceinline__ void find(const ScoredParams& P) {
     for (; u < P.num_units; u = unit_of(++r)) {
-      x = decode_unit(P, u);
+      x = decode_unit(P, u, order);
       if (x.t.jb < x.t.je) {
         j = DOWN ? x.t.je - 1 : x.t.jb;
         first = true;
@@ -150,7 +151,8 @@ struct Walk {
     }
     done = true;
   }
-  __device__ __forceinline__ void begin(const ScoredParams& P) {
+  __device__ __forceinline__ void begin(const ScoredParams& P, const uint16_t* tiles) {
+    order = tiles;
     r = 0;
     u = unit_of(0);
     n = nu = 0;
@@ -302,6 +304,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   pdl_wait();
   pdl_launch_dependents();
+  uint16_t* const order_smem = reinterpret_cast<uint16_t*>(ctrl + 512);
+  const uint16_t* const order =
+      order_tiles(P.mask, P.q_blocks, P.T, P.causal, P.num_units <= static_cast<int32_t>(gridDim.x),
+                  order_smem, order_smem + kOrderTiles);
 
   constexpr bool DOWN = MODE == kBias || MODE == kCapAny;
   Walk<DOWN> w;
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------- Q, K and V loads
         // K runs NK blocks ahead of V: a walk each.
         Walk<DOWN> a;
-        a.begin(P);
+        a.begin(P, order);
         int64_t nk = 0;
         uint32_t nv = 0, units = 0;
         auto load_k = [&]() {
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
         bool ok = true;
         for (int i = 0; ok && i < NK; ++i) ok = load_k();
-        for (w.begin(P); ok && !w.done; w.next(P)) {
+        for (w.begin(P, order); ok && !w.done; w.next(P)) {
           if (!wait_asleep(v_empty(w.n), ((w.n / NV) & 1) ^ 1u, abort_flag, P.wait, kErrWaitEmpty)) break;
           mbar_arrive_expect_tx(v_full(w.n), TILE_BYTES);
           for (int c = 0; c < 2; ++c)
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         auto await = [&](uint32_t bar, uint32_t parity, unsigned code) {
           return __all_sync(0xffffffffu, wait_asleep(bar, parity, abort_flag, P.wait, code)) != 0;
         };
-        for (w.begin(P); !w.done; w.next(P)) {
+        for (w.begin(P, order); !w.done; w.next(P)) {
           if ((w.first && !await(q_full, w.nu & 1, kErrWaitFull)) ||
               !await(k_full(w.n), (w.n / NK) & 1, kErrWaitFull) ||
               // the buffer's last probabilities have been used
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         auto await = [&](uint32_t bar, uint32_t parity, unsigned code) {
           return __all_sync(0xffffffffu, wait_asleep(bar, parity, abort_flag, P.wait, code)) != 0;
         };
-        for (w.begin(P); !w.done; w.next(P)) {
+        for (w.begin(P, order); !w.done; w.next(P)) {
           if ((w.first && w.nu > 0 &&
                !await(o_empty, (w.nu - 1) & 1, kErrWaitAttn)) ||
               !await(v_seen(w.n), (w.n / NV) & 1, kErrWaitFull) ||
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
     } else {
       // ----------------------------------- values in blocks that a mask cuts
-      for (w.begin(P); !w.done; w.next(P)) {
+      for (w.begin(P, order); !w.done; w.next(P)) {
         bool ok = wait_asleep(v_full(w.n), (w.n / NV) & 1, abort_flag, P.wait, kErrWaitFull);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool started = g == 1;             // a block came before (of either group)
     int32_t r = 0;
     for (int32_t u = unit_of(0); ok && u < P.num_units; u = unit_of(++r)) {
-      const Unit x = decode_unit(P, u);
+      const Unit x = decode_unit(P, u, order);
       const int32_t blocks = x.t.je - x.t.jb;
       if (blocks <= 0) continue;
       const int32_t q = x.qb * BQ + row;
