@@ -679,7 +679,8 @@ tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void*
  *   workspace  tp_attention_scored_backward_workspace_size(...) bytes,
  *              256-byte aligned
  * P and dS are rounded to bf16 before their products, the gradients once at
- * the end; sums are fp32 in a fixed order (reproducible).
+ * the end; sums are fp32 in a fixed order (reproducible).  A row that sees one
+ * key has exactly no gradient through its score.
  */
 tp_status tp_attention_scored_backward(const void* Q, const void* K, const void* V, const void* O,
                                        const float* LSE, const void* dO, void* dQ, void* dK,

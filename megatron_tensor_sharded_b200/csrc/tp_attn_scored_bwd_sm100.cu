@@ -17,8 +17,13 @@
 // Scores and probabilities are recomputed in both: seven products a tile
 // instead of the five that one kernel with atomic adds to dQ would need, in
 // exchange for the same bits on every run, no fp32 dQ in memory and no pass
-// that converts it.  Both are bound by the tensor cores (4 and 3 products of
-// 128 x 128 x 128 a tile) with the softmax's arithmetic beside them.
+// that converts it.  Both are bound by a step's chain of the tensor cores' work
+// (4 and 3 products of 128 x 128 x 128 a tile, 57% and 50% of the time) and the
+// softmax's arithmetic, which overlap as far as TMEM's 512 columns allow.
+// 4096 causal tokens, 32 heads, cap: 269 and 229 us; with D, 580 in all.
+//
+// D comes from O as it was stored: dQ and dK are 0.0027 off in the 2-norm where
+// an fp32 O would leave the 0.0024 of P's, dS's and their own rounding.
 //
 // dkv computes the transposed tiles S^T = K Q^T and dP^T = V dO^T: a thread
 // then owns a key row, and P^T and dS^T, left in TMEM as bf16, are the A
@@ -26,11 +31,11 @@
 // that S^T and dP^T read: no operand is transposed or written to shared
 // memory.  dq likewise: dQ += dS K.  The sixteen arithmetic warps split a tile
 // by column quarters; each quarter's bf16 result goes over the first half of
-// its own scores, so the quarters never wait for one another.  S^T is free as soon as the warps hold it in registers,
-// since P^T and dS^T both go over dP^T: the next S^T runs while they form P^T,
-// and dV, dK and the next dP^T while they form the next P^T.  (With P^T over
-// S^T, the next S^T waited for dV: 4150 clocks a step against 2048 of
-// products.)
+// its own scores, so the quarters never wait for one another.  S^T is free as
+// soon as the warps hold it in registers, since P^T and dS^T both go over dP^T:
+// the next S^T runs while they form P^T, and dV, dK and the next dP^T while
+// they form the next P^T.  (With P^T over S^T, the next S^T waited for dV: 653
+// us for the whole backward against 624 when that was changed.)
 //
 // A query that sees one key has P = 1 and dS = 0 exactly; dP - D leaves the
 // rounding of two sums there, so w is set to 0 (times 0: a NaN stays).
@@ -345,10 +350,12 @@ __global__ void __launch_bounds__(256)
 // one that it begins), which dkv_join_kernel adds in the order of the CTAs.
 // Handed out whole instead, units leave SMs idle where there are few of them or
 // where documents make them differ: 369 us for the whole backward against 244
-// for 1999 tokens of five documents, 64 query and 8 key/value heads.  But a cut
+// (when this was chosen) for 1999 tokens of five documents, 64 query and 8
+// key/value heads.  But a cut
 // costs a store, a load and a sum of 128 KB, and where the CTAs take many units
 // each, in turns from the two ends, their sums are even anyway: P.whole
-// (kWholeUnits a CTA, no mask): 648 us against 616 for 4096 tokens and 32 heads.
+// (kWholeUnits a CTA, no mask): 616 us against 648 cut, for 4096 tokens and 32
+// heads.
 __device__ __forceinline__ int2 key_tiles(const BwdParams& P, int32_t kb) {
   if (P.mask.rows != nullptr) return P.mask.k_tiles[kb];
   return make_int2(P.causal ? kb : 0, P.tiles);

@@ -19,8 +19,9 @@
 // the scores they came from, as the A operand of P V.  A tensor-core
 // instruction is issued only when the pipe takes it, so whatever else the
 // issuing thread does adds to the products' time (90 clocks for a commit and a
-// wait after eight of them): Q K^T and P V have a thread each, and one's waits
-// run beside the other's products.
+// wait after eight of them): Q K^T and P V have a warp each, and one's waits
+// run beside the other's products.  4096 causal tokens, 64 heads, cap: 355 us,
+// 775 TFLOP/s; 2300 clocks a tile and block, of 1040 of products.
 // Roles (640 threads): warp 0 loads Q, K (two slots) and V (three), warp 1
 // issues Q K^T, warp 3 P V, warp 2 looks at V where a mask cuts a block, warps
 // 4..11 and 12..19 are the two softmax groups.

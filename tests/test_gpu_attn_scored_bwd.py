@@ -255,3 +255,64 @@ def test_a_query_with_one_key_has_no_gradient(case):
     dev[1][:, one.nonzero()[0, 0]] = float("nan")
     dQ, dK, dV = _call(case, dev, score, O, LSE)
     assert torch.all(torch.isnan(dQ[:, one.nonzero()[0, 0]]))
+
+
+def test_many_tiles_of_documents():
+    """More query tiles than are sorted: a document among many gives what it
+    gives alone, O within both calls' roundings (2 u of sum P|v| each), the
+    gradients within 8 u in the 2-norm (4 u each, see above)."""
+    T, h = 66000, 2
+    off = list(range(0, T - 700, 517)) + [T - 30]
+    n = len(off) // 2
+    rng = np.random.default_rng(3)
+    (Q, _), (K, _), (V, _), (dO, _) = (S.bf16(rng, 1, T, w * 128) for w in (h, 1, 1, h))
+    slopes = torch.tensor([0.5, 0.03], device="cuda")
+
+    def run(lo, hi, offsets):
+        t = hi - lo
+        x = [y[:, lo:hi].contiguous() for y in (Q, K, V, dO)]
+        size = tp.tp_attention_mask_size(t)
+        mask = torch.empty(size, dtype=torch.uint8, device="cuda")
+        tp.tp_attention_mask(torch.tensor(offsets, dtype=torch.int32, device="cuda"), len(offsets) - 1, None, True, mask, size, t)
+        score = tp.score_params(slopes=slopes, mask=mask, causal=True)
+        O, LSE = torch.zeros_like(x[0]), torch.zeros(1, h, t, device="cuda")
+        tp.tp_attention_scored(*x[:3], O, LSE, t, 1, h, 1, 128, score)
+        g = [torch.zeros_like(y) for y in x[:3]]
+        w = tp.tp_attention_scored_backward_workspace_size(t, 1, h, 1, 128)
+        tp.tp_attention_scored_backward(*x[:3], O, LSE, x[3], *g, torch.empty(w, dtype=torch.uint8, device="cuda"), w, t, 1, h, 1, 128, score)
+        tp.tp_sync_status()
+        return O, g
+
+    O, g = run(0, T, off)
+    for d in (0, n, len(off) - 2):
+        lo, hi = off[d], off[d + 1]
+        O1, g1 = run(lo, hi, [0, hi - lo])
+        assert (O[:, lo:hi].float() - O1.float()).abs().max() <= 4 * S.U * V.float().abs().max()
+        for a, b in zip(g, g1):
+            a, b = a[:, lo:hi].double(), b.double()
+            assert (a - b).norm() <= 8 * S.U * b.norm()
+    assert all(torch.all(x[:, T - 30:] == 0) for x in [O] + g)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its own workspace and outputs: the bits of the
+    calls one after the other."""
+    cases = [dict(p=1, T=700, h=8, hkv=2, cap=50.0), dict(p=2, T=520, h=8, hkv=4, off=[0, 130, 470], slopes=1.0)]
+    sets = [_setup(c) for c in cases]
+    alone = [_call(c, s[0], s[3], s[6], s[7]) for c, s in zip(cases, sets)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for c, s, st in zip(cases, sets, streams):
+        p, T, h, hkv = c["p"], c["T"], c["h"], c["hkv"]
+        with torch.cuda.stream(st):
+            g = [torch.full_like(x, 7.0) for x in s[0][:3]]
+            n = tp.tp_attention_scored_backward_workspace_size(T, p, h, hkv, 128)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            for _ in range(4):
+                tp.tp_attention_scored_backward(*s[0][:3], s[6], s[7], s[0][3], *g, ws, n, T, p, h, hkv, 128, s[3])
+        got.append((g, ws))
+    torch.cuda.synchronize()
+    tp.tp_sync_status()
+    for a, (g, _) in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, g))
