@@ -84,7 +84,10 @@ constexpr uint32_t IDESC_KN = idesc_bf16_f32(BT, DH, 0, 1);   // A in TMEM, B ro
 template <bool CAP>
 constexpr int kPolyPairs = CAP ? 0 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kUnitCost = 2;                  // of a dkv unit beside its steps, in steps
+// A dkv unit's loads, start and stores, in steps (1999 tokens of five documents,
+// 64/8 heads, whole backward: 2 230 us, 4 226, 6 226, 8 228; a smaller one 49,
+// 42, 41, 41).
+constexpr int kUnitCost = 4;
 constexpr int kWholeUnits = 6;                // units a CTA from which none is cut
 constexpr int kCut = 1, kFirst = 2, kLast = 4, kEnd = 8;   // a step: cut by a mask; its unit's; the share's last
 constexpr int PART_FLOATS = 2 * BT * DH;      // dV and dK of a key tile
@@ -1309,7 +1312,8 @@ tp_status launch_bwd(const LaunchCtx& c, BwdParams prm, const ScoreCall& a, cons
 }  // namespace
 
 // CTAs that share the steps of dK and dV: one an SM, fewer where they would get
-// less than two steps each even without a mask.
+// less than two steps each even without a mask (four instead of two: 28 us to 37
+// for a call of such a size).
 int64_t score_dkv_ctas(const ScoreCall& a) {
   const int64_t tiles = ceil_div(a.T, BT);
   const int64_t steps = static_cast<int64_t>(a.p) * a.hq * (a.causal ? tiles * (tiles + 1) / 2 : tiles * tiles);
