@@ -73,7 +73,11 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // fitted the same way (relative error of the fit 7.5e-8, in fp32 2.1e-7: the
 // log of a row's sum is kept in fp32).  NAN_SAFE: NaN for a NaN -- the power
 // of two is multiplied in (its exponent field is built apart), where adding
-// to the bits of a NaN would give a number.
+// to the bits of a NaN would give a number.  Otherwise the clamp lies at -127,
+// where the polynomial is 1 + 2^-23 and the bits come to 2^-149: -inf gives a
+// number that is 0 as bf16.  (2^-126 is not: a key that a row does not see
+// would add 2^-126 times its value, which may be 2^127.)  Between -127 and
+// -126 the result lies between 0 and 2^-126.
 template <bool NAN_SAFE>
 __device__ __forceinline__ uint64_t exp2_poly5(uint64_t x2) {
   float x0, x1;
@@ -81,7 +85,7 @@ __device__ __forceinline__ uint64_t exp2_poly5(uint64_t x2) {
   if (NAN_SAFE)
     x2 = f2_pack(max3_nan(x0, -126.0f, -126.0f), max3_nan(x1, -126.0f, -126.0f));
   else
-    x2 = f2_pack(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+    x2 = f2_pack(fmaxf(x0, -127.0f), fmaxf(x1, -127.0f));
   const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);
   const uint64_t t = f2_add(x2, magic);
   const uint64_t n = f2_add(t, f2_pack(-12582912.0f, -12582912.0f));
