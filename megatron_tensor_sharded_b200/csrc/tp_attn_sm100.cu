@@ -164,7 +164,7 @@ __device__ __forceinline__ float softmax_one_pass(uint32_t tS, float scale, floa
       const uint64_t xa = f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2);
       float a0, a1;
       if ((e / 2) % 8 < POLY_PAIRS) {
-        f2_unpack(exp2_poly2(xa), a0, a1);
+        f2_unpack(exp2_poly2<MASK>(xa), a0, a1);
       } else {
         float x0, x1;
         f2_unpack(xa, x0, x1);
@@ -474,7 +474,7 @@ __global__ void exp2_poly_probe_kernel(const float* __restrict__ x, float* __res
   const float x0 = x[i];
   const float x1 = i + 1 < n ? x[i + 1] : 0.0f;
   float y0, y1;
-  f2_unpack(exp2_poly2(f2_pack(x0, x1)), y0, y1);
+  f2_unpack(exp2_poly2<false>(f2_pack(x0, x1)), y0, y1);
   y[i] = y0;
   if (i + 1 < n) y[i + 1] = y1;
 }

@@ -41,12 +41,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // coefficients were fitted to minimise the relative error on [-1/2, 1/2]
 // (iteratively reweighted least squares; max relative error of the fit
 // 2.6e-6, of the fp32 evaluation below at most 2.7e-6 on [-126, 0]), and n
-// added to the exponent field.  x is clamped to >= -126 (the probabilities
-// are bf16, so 2^-126 and 0 are the same to them).  Two lanes per call.
+// added to the exponent field.  x is clamped to >= -126, or, MASKED, to
+// -126.9999: the polynomial is 1 + 6.9e-5 there and the bits come to 8e-43, so
+// -inf gives a number that is 0 as bf16 (2^-126 is not, and would count beside
+// a value of 2^127).  (At -127 itself the polynomial is just below 1 and the
+// bits would be a NaN's.)  Two lanes per call.
+template <bool MASKED>
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
+  constexpr float kLeast = MASKED ? -126.9999f : -126.0f;
   float x0, x1;
   f2_unpack(x2, x0, x1);
-  x2 = f2_pack(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+  x2 = f2_pack(fmaxf(x0, kLeast), fmaxf(x1, kLeast));
   const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);
   const uint64_t t = f2_add(x2, magic);
   const uint64_t n = f2_add(t, f2_pack(-12582912.0f, -12582912.0f));

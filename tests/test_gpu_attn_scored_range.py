@@ -5,6 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+import megatron_tensor_sharded_b200 as tp
+import scored_util as S
+from oracle import attn_oracle as A
 from test_gpu_attn_scored import _check, _run
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +41,22 @@ def test_unseen_finite_values_add_nothing(mask, bad, fine, opts):
     rows = np.zeros(300, bool)
     rows[fine[0]:fine[1]] = True
     _check(case, host, slopes, seen, inside, O, LSE, rows=rows)
+
+
+@pytest.mark.parametrize("at", [1, 70, 128, 200, 299])
+def test_later_tokens_add_nothing_to_plain_heads(at):
+    """tp_attention_heads, causal, with the largest finite keys and values from
+    token `at` on."""
+    p, T, h, hkv = 1, 300, 2, 1
+    rng = np.random.default_rng(at)
+    (Q, Qh), (K, Kh), (V, Vh) = (S.bf16(rng, p, T, n * 128) for n in (h, hkv, hkv))
+    K[:, at:], V[:, at:] = -BIG, BIG
+    O = torch.zeros_like(Q)
+    tp.tp_attention_heads(Q, K, V, O, T, p, h, hkv, 128, True)
+    tp.tp_sync_status()
+    for j in range(h):
+        q, k, v = S.head(Qh, 0, j), S.head(Kh, 0, 0), S.head(Vh, 0, 0)
+        want, _ = A.scored_head(q, k, v, np.tri(T, dtype=bool), 128 ** -0.5)
+        E = S.score_error(q, k, 128 ** -0.5, 0.0, 0.0, T)
+        tol = (S.U + 2 * E) * np.abs(v).max() + S.U * np.abs(want)
+        assert np.all((np.abs(O[0, :, j * 128:j * 128 + 128].double().cpu().numpy() - want) <= tol)[:at])
