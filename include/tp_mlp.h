@@ -658,9 +658,10 @@ size_t tp_attention_mask_size(int64_t T);
  *   LSE    [p][n_heads/p][T] fp32 or NULL (the backward call needs it)
  *   score  NULL: no options (every row sees every key)
  * A key adds nothing to a row that does not see it, whatever K and V hold
- * there (infinities and NaN too).  Scores, maxima, sums and the accumulator
- * are fp32; probabilities are rounded to bf16 before P V and O once at the
- * end.  The results are reproducible.
+ * there (infinities and NaN too).  A row that sees a score of +inf or NaN
+ * gives NaN (LSE +inf or NaN), one whose scores are all -inf 0 (LSE -inf).
+ * Scores, maxima, sums and the accumulator are fp32; probabilities are rounded
+ * to bf16 before P V and O once at the end.  The results are reproducible.
  */
 tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
                               int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,

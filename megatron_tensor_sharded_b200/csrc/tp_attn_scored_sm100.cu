@@ -491,7 +491,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         L += mi == M ? li : li * ex2(mi - M);
         mark += e[(8 + i) * BQ];
       }
-      const float inv_l = mark != 0.0f ? NAN : L == 0.0f ? 0.0f : 1.0f / L;
+      // (M = inf: some score is, the softmax is NaN and its polynomial 2^x would
+      // hide it; M = -inf: all are, and nothing has a weight)
+      const bool none = L == 0.0f || (HAS_MAX && M == -INFINITY), over = HAS_MAX && M == INFINITY;
+      const float inv_l = mark != 0.0f || over ? NAN : none ? 0.0f : 1.0f / L;
       uint32_t v[32];
       tmem_ld_32x32b_x32(tO + part * 32, v);
       tmem_ld_wait();
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           *reinterpret_cast<uint4*>(dst + q * 8) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         if (part == 0 && P.LSE != nullptr)
-          P.LSE[p_lse] = L == 0.0f ? -INFINITY : 0.6931471805599453f * M + logf(L);
+          P.LSE[p_lse] = over ? INFINITY : none ? -INFINITY : 0.6931471805599453f * M + logf(L);
       }
       return true;
     };

@@ -60,3 +60,38 @@ def test_later_tokens_add_nothing_to_plain_heads(at):
         E = S.score_error(q, k, 128 ** -0.5, 0.0, 0.0, T)
         tol = (S.U + 2 * E) * np.abs(v).max() + S.U * np.abs(want)
         assert np.all((np.abs(O[0, :, j * 128:j * 128 + 128].double().cpu().numpy() - want) <= tol)[:at])
+
+
+@pytest.mark.parametrize("slope", [0.0, 0.01], ids=["plain", "bias"])
+@pytest.mark.parametrize("key", [0, 2, 4, 15, 16, 19, 40, 131])
+def test_infinite_scores(key, slope):
+    """A key whose score is +inf: softmax is NaN and the log of the sum +inf in
+    the rows that see it; one whose score is -inf has no weight, whatever its
+    value."""
+    T = 200
+    rng = np.random.default_rng(key)
+    (Q, Qh), (K, Kh), (V, Vh) = (S.bf16(rng, 1, T, 128) for _ in range(3))
+    Q[0, :, 5], Qh[0, :, 5] = 1.0, 1.0
+    sl = torch.tensor([slope], device="cuda") if slope else None
+    score = tp.score_params(slopes=sl, causal=True)
+    for value in (np.inf, -np.inf):
+        K2, V2 = K.clone(), V.clone()
+        K2[0, key, 5] = value
+        V2[0, key] = 1.0 if value > 0 else BIG
+        O, LSE = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+        tp.tp_attention_scored(Q, K2, V2, O, LSE, T, 1, 1, 1, 128, score)
+        tp.tp_sync_status()
+        O, LSE = O[0].double().cpu().numpy(), LSE[0, 0].double().cpu().numpy()
+        seen = np.tri(T, dtype=bool)
+        rows = np.arange(T) < key if value > 0 else np.arange(T) != key
+        if value > 0:
+            assert np.isnan(O[key:]).all() and (LSE[key:] == np.inf).all()
+        else:
+            seen[:, key] = False
+            if key == 0:
+                assert LSE[0] == -np.inf
+        want, lse = A.scored_head(Qh[0], Kh[0], Vh[0], seen, 128 ** -0.5, 0.0, slope)
+        E = S.score_error(Qh[0], Kh[0], 128 ** -0.5, 0.0, slope, T)
+        tol = (S.U + 2 * E) * np.abs(Vh).max() + S.U * np.abs(want)
+        assert np.all((np.abs(O - want) <= tol)[rows])
+        assert np.all(np.abs(LSE[rows] - lse[rows]) <= E + 2.0 ** -22 * np.abs(lse[rows]))
