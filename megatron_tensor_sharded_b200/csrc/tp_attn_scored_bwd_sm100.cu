@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(qd_empty, 1);
     for (int s = 0; s < NA; ++s) {
       mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
+      mbar_init(k_empty(s), 3);   // the issuing thread's commit, warps 2 and 3
       mbar_init(k_seen(s), 64);
     }
     for (int s = 0; s < NB; ++s) {
@@ -1180,6 +1180,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_arrive(k_seen(looked));
             ++looked;
           }
+          // (the slot is held for these warps in every block, as they wait for
+          // every block's load: k_full two loads on has the parity of the phase
+          // that they wait for, and would keep a late warp waiting)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_empty(n));
         }
       }
     }

@@ -316,3 +316,17 @@ def test_two_calls_at_once():
     tp.tp_sync_status()
     for a, (g, _) in zip(alone, got):
         assert all(torch.equal(x, y) for x, y in zip(a, g))
+
+
+@pytest.mark.parametrize("case", [
+    dict(p=1, T=2300, h=20, hkv=20, causal=False, cap=30.0),
+    dict(p=2, T=2300, h=20, hkv=4, off=[0, 2200]),
+], ids=["full", "causal"])
+def test_long_runs_of_blocks_that_no_mask_cuts(case):
+    """Many key blocks of one query tile in a row that are seen whole, several
+    such tiles a CTA: every wait ends, and the same bits again and again."""
+    dev, host, slopes, score, seen, inside, O, LSE = _setup(case)
+    grads = _call(case, dev, score, O, LSE)
+    _check(case, host, slopes, seen, inside, O, LSE, grads, kv_heads={(0, 0)})
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(grads, _call(case, dev, score, O, LSE)))
