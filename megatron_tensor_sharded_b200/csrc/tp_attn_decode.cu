@@ -34,6 +34,7 @@
 #include "tp_device.cuh"
 #include "tp_internal.h"
 #include "tp_launch.cuh"
+#include "tp_score.cuh"
 #include "tp_score.h"
 #include "tp_softmax.cuh"
 
@@ -162,7 +163,7 @@ __device__ __forceinline__ void advance(const DecodeParams& P, Place& x) {
 }
 
 // NT: 8-head column tiles of an item.
-template <bool CAP, bool BIAS, int NT>
+template <int CAP, bool BIAS, int NT>
 __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
     decode_kernel(const __grid_constant__ DecodeParams P) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -317,9 +318,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float z;
-        if (CAP) {
-          const float x = 1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s[t][e]) * P.s.two_x));
-          z = P.s.cap_log2 * copysignf(x, s[t][e]);
+        if (CAP != kNoCap) {
+          z = cap_score<CAP == kFineCap>(s[t][e], P.s);
         } else {
           z = s[t][e] * P.s.scale_log2;
         }
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) decode_join_kernel(const __grid_
   }
 }
 
-template <bool CAP, bool BIAS, int NT>
+template <int CAP, bool BIAS, int NT>
 tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
   static uint64_t attr_epoch[64] = {};
   static std::mutex mu;
@@ -600,6 +600,12 @@ tp_status launch_decode(const LaunchCtx& c, const DecodeParams& prm) {
     return TP_ERR_CUDA;
   }
   return TP_OK;
+}
+
+template <int CAP, int NT>
+tp_status launch_form(const LaunchCtx& c, const DecodeParams& prm) {
+  if (prm.slopes != nullptr) return launch_decode<CAP, true, NT>(c, prm);
+  return launch_decode<CAP, false, NT>(c, prm);
 }
 
 }  // namespace
@@ -644,17 +650,15 @@ tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a) {
   prm.s = score_consts(a.scale, a.cap);
   prm.err = c.err_word;
   prm.ctas = static_cast<int32_t>(decode_ctas(c.num_sms, a.B, a.capacity, a.p, a.hq, a.hkv));
-  const bool cap = a.cap > 0.0f, bias = a.slopes != nullptr;
+  const int cap = cap_form(prm.s.cap_log2);
   if (prm.rows == 8) {
-    if (cap && bias) return launch_decode<true, true, 1>(c, prm);
-    if (cap) return launch_decode<true, false, 1>(c, prm);
-    if (bias) return launch_decode<false, true, 1>(c, prm);
-    return launch_decode<false, false, 1>(c, prm);
+    if (cap == kFineCap) return launch_form<kFineCap, 1>(c, prm);
+    if (cap == kCoarseCap) return launch_form<kCoarseCap, 1>(c, prm);
+    return launch_form<kNoCap, 1>(c, prm);
   }
-  if (cap && bias) return launch_decode<true, true, 2>(c, prm);
-  if (cap) return launch_decode<true, false, 2>(c, prm);
-  if (bias) return launch_decode<false, true, 2>(c, prm);
-  return launch_decode<false, false, 2>(c, prm);
+  if (cap == kFineCap) return launch_form<kFineCap, 2>(c, prm);
+  if (cap == kCoarseCap) return launch_form<kCoarseCap, 2>(c, prm);
+  return launch_form<kNoCap, 2>(c, prm);
 }
 
 }  // namespace tpk

@@ -81,7 +81,7 @@ constexpr uint32_t IDESC_KN = idesc_bf16_f32(BT, DH, 0, 1);   // A in TMEM, B ro
 // Of every eight pairs of probabilities, those whose 2^x runs on the FMA pipe:
 // none with the cap, whose own arithmetic there (11 clocks of a scheduler an
 // element against the MUFU unit's 8) is the longer already.
-template <bool CAP>
+template <int CAP>
 constexpr int kPolyPairs = CAP ? 0 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
 // A dkv unit's loads, start and stores, in steps (1999 tokens of five documents,
@@ -142,12 +142,12 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 
 // 32 raw products -> P as bf16 pairs in pk and w = P (1 - tanh^2).  nl(e):
 // -LSE log2 e of columns e .. e + 3; seen(e): whether the pair counts.
-template <bool CAP, bool BIAS, typename NegLse, typename Seen>
+template <int CAP, bool BIAS, typename NegLse, typename Seen>
 __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], uint32_t (&pk)[16],
                                            const BwdParams& P, float slope2, float dist0, int side,
                                            bool cut, NegLse nl, Seen seen) {
   if (CAP) {
-    cap_chunk(v, P.s);
+    cap_chunk<CAP == kFineCap>(v, P.s);
     const uint64_t ic = f2_pack(P.neg_inv_cap2, P.neg_inv_cap2), one = f2_pack(1.0f, 1.0f);
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -493,7 +493,7 @@ __device__ __forceinline__ int4 find_share(const BwdParams& P, int lane) {
   return found;
 }
 
-template <bool CAP, bool BIAS>
+template <int CAP, bool BIAS>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_scored_dkv_kernel(const __grid_constant__ CUtensorMap mapQ,
                          const __grid_constant__ CUtensorMap mapK,
@@ -952,7 +952,7 @@ __device__ __forceinline__ QueryUnit query_unit(const BwdParams& P, int32_t u, c
   return x;
 }
 
-template <bool CAP, bool BIAS>
+template <int CAP, bool BIAS>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_scored_dq_kernel(const __grid_constant__ CUtensorMap mapQ,
                         const __grid_constant__ CUtensorMap mapK,
@@ -1268,7 +1268,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-template <bool CAP, bool BIAS>
+template <int CAP, bool BIAS>
 tp_status launch_bwd(const LaunchCtx& c, BwdParams prm, const ScoreCall& a, const CUtensorMap& mQ,
                      const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mdO) {
   static uint64_t attr_epoch[64] = {};
@@ -1312,6 +1312,13 @@ tp_status launch_bwd(const LaunchCtx& c, BwdParams prm, const ScoreCall& a, cons
     return TP_ERR_CUDA;
   }
   return TP_OK;
+}
+
+template <int CAP>
+tp_status launch_form(const LaunchCtx& c, const BwdParams& prm, const ScoreCall& a, const CUtensorMap& mQ,
+                      const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mdO) {
+  if (prm.slopes != nullptr) return launch_bwd<CAP, true>(c, prm, a, mQ, mK, mV, mdO);
+  return launch_bwd<CAP, false>(c, prm, a, mQ, mK, mV, mdO);
 }
 
 }  // namespace
@@ -1373,11 +1380,10 @@ tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a) {
   prm.wait.err = c.err_word;
   prm.wait.timeout_ns = c.timeout_ns;
   prm.debug_drop = c.debug_drop;
-  const bool cap = a.cap > 0.0f, bias = a.slopes != nullptr;
-  if (cap && bias) return launch_bwd<true, true>(c, prm, a, mQ, mK, mV, mdO);
-  if (cap) return launch_bwd<true, false>(c, prm, a, mQ, mK, mV, mdO);
-  if (bias) return launch_bwd<false, true>(c, prm, a, mQ, mK, mV, mdO);
-  return launch_bwd<false, false>(c, prm, a, mQ, mK, mV, mdO);
+  const int cap = cap_form(prm.s.cap_log2);
+  if (cap == kFineCap) return launch_form<kFineCap>(c, prm, a, mQ, mK, mV, mdO);
+  if (cap == kCoarseCap) return launch_form<kCoarseCap>(c, prm, a, mQ, mK, mV, mdO);
+  return launch_form<kNoCap>(c, prm, a, mQ, mK, mV, mdO);
 }
 
 }  // namespace tpk

@@ -92,7 +92,9 @@ constexpr uint32_t O_COL0 = NS * BKV, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float kBoundLog2 = 80.0f;          // |z| in log2 that needs no running maximum
 
-enum { kPlain = 0, kBias = 1, kCap = 2, kCapAny = 3 };   // kCap: no bias, bounded
+// kCap: no bias, bounded; kCapAny: with a maximum; kCapFine: the same past kCoarseCapLog2
+enum { kPlain = 0, kBias = 1, kCap = 2, kCapAny = 3, kCapFine = 4 };
+static_assert(kBoundLog2 <= kCoarseCapLog2, "kCap takes the coarse form");
 
 struct ScoredParams {
   int32_t T, p, hq, hkv, group, q_blocks, num_units, causal;
@@ -177,7 +179,7 @@ struct Walk {
 // with the cap and 2 to 3 without, 9 more where 2^x is there too, and the MUFU
 // unit 8 where it is not.
 template <int MODE>
-constexpr int kPolyPairs = MODE == kCap || MODE == kCapAny ? 0 : 2;
+constexpr int kPolyPairs = MODE >= kCap ? 0 : 2;
 
 // Probabilities of 32 scores: bf16 pairs into pk, fp32 sums into sum2.
 // SCALE: x = v * sc + off, else v holds x itself.
@@ -210,8 +212,8 @@ __device__ __forceinline__ void score_chunk(uint32_t (&v)[32], const ScoreConsts
                                             float dist0, int side, bool whole, int32_t rl,
                                             int32_t rh, bool& lost) {
   bool slow = false;
-  if (MODE == kCap || MODE == kCapAny) slow = cap_chunk(v, S);
-  if (MODE == kBias || MODE == kCapAny)
+  if (MODE >= kCap) slow = cap_chunk<MODE == kCapFine>(v, S);
+  if (MODE == kBias || MODE >= kCapAny)
     bias_chunk<MODE == kBias>(v, S.scale_log2, slope2, dist0, side);
   if (!whole) mask_chunk(v, rl, rh);
   if (MODE == kCap && slow) {
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       order_tiles(P.mask, P.q_blocks, P.T, P.causal, P.num_units <= static_cast<int32_t>(gridDim.x),
                   order_smem, order_smem + kOrderTiles);
 
-  constexpr bool DOWN = MODE == kBias || MODE == kCapAny;
+  constexpr bool DOWN = MODE == kBias || MODE >= kCapAny;
   Walk<DOWN> w;
   // 96 registers a thread at launch: 128 x 64 + 512 x 104 <= 640 x 96
   if (warp < 4) {
@@ -530,7 +532,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int32_t q = x.qb * BQ + row;
       const int2 seen = row_span(P.mask, q, P.T, P.causal);
       float slope2 = 0.0f;
-      if (MODE == kBias || MODE == kCapAny)
+      if (MODE == kBias || MODE >= kCapAny)
         slope2 = P.slopes != nullptr ? 1.4426950408889634f * P.slopes[x.shard * P.hq + x.head] : 0.0f;
       for (int32_t i = (static_cast<uint32_t>(g) ^ parity0) & 1; i < blocks; i += 2) {
         // (a group that enters the unit with its second block does the previous
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int32_t rl = seen.x - key0, rh = seen.y - key0;
         float dist0 = 0.0f;
         int side = 0;
-        if (MODE == kBias || MODE == kCapAny) {
+        if (MODE == kBias || MODE >= kCapAny) {
           dist0 = static_cast<float>(key0 - q);
           side = j * BKV + BKV - 1 <= x.qb * BQ ? -1 : j * BKV >= x.qb * BQ + BQ - 1 ? 1 : 0;
         }
@@ -572,9 +574,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               acc[0] = max3_nan(acc[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
               acc[1] = max3_nan(acc[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
             }
-            if (MODE == kCapAny) tmem_st_32x32b_x32(tS + c * 32, v);   // (else computed again below)
+            if (MODE >= kCapAny) tmem_st_32x32b_x32(tS + c * 32, v);   // (else computed again below)
           }
-          if (MODE == kCapAny) tmem_st_wait();
+          if (MODE >= kCapAny) tmem_st_wait();
           float m_cand = max3_nan(acc[0], acc[1], acc[1]);
           // the other group's maximum first: its arrival also says that this
           // group's last exchange has been read
@@ -816,6 +818,7 @@ tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a) {
   prm.debug_drop = c.debug_drop;
   if (a.cap > 0.0f) {
     if (a.slopes == nullptr && prm.s.cap_log2 <= kBoundLog2) return launch_mode<kCap>(c, prm, mQ, mK, mV);
+    if (cap_form(prm.s.cap_log2) == kFineCap) return launch_mode<kCapFine>(c, prm, mQ, mK, mV);
     return launch_mode<kCapAny>(c, prm, mQ, mK, mV);
   }
   if (a.slopes != nullptr) return launch_mode<kBias>(c, prm, mQ, mK, mV);

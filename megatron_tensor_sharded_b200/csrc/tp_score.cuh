@@ -83,8 +83,24 @@ __device__ __forceinline__ int2 key_span(const MaskPlan& m, int32_t k, int32_t T
   return make_int2(causal ? k : 0, T);
 }
 
+// A raw product -> its capped score in log2 units, of any size.  The MUFU form
+// is off by up to 2^-21 of the cap in every score: less than the products' own
+// rounding at caps of tens, 0.2 at a cap of 10^6.  FINE: the polynomial where
+// |scale s| <= cap/2, where that is what is lost (eight instructions more).
+template <bool FINE>
+__device__ __forceinline__ float cap_score(float s, const ScoreConsts& S) {
+  const float far = copysignf(1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s) * S.two_x)), s);
+  if (!FINE) return S.cap_log2 * far;
+  constexpr float c0 = static_cast<float>(kTanh[0]), c1 = static_cast<float>(kTanh[1]);
+  constexpr float c2 = static_cast<float>(kTanh[2]), c3 = static_cast<float>(kTanh[3]);
+  const float x = s * S.x_of_s, u = x * x;
+  const float near = x * fmaf(u, fmaf(u, fmaf(u, c3, c2), c1), c0);
+  return S.cap_log2 * (fabsf(x) <= 0.5f ? near : far);
+}
+
 // 32 raw products -> capped scores in log2 units.  True where the warp took
-// the MUFU form (some row's |scale s| > cap/2, or a NaN).
+// the form of cap_score (some row's |scale s| > cap/2, or a NaN).
+template <bool FINE>
 __device__ __forceinline__ bool cap_chunk(uint32_t* v, const ScoreConsts& S) {
   float mx[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -108,11 +124,7 @@ __device__ __forceinline__ bool cap_chunk(uint32_t* v, const ScoreConsts& S) {
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float s = __uint_as_float(v[e]);
-      const float t = 1.0f - 2.0f * rcp_approx(1.0f + ex2(fabsf(s) * S.two_x));
-      v[e] = __float_as_uint(S.cap_log2 * copysignf(t, s));
-    }
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(cap_score<FINE>(__uint_as_float(v[e]), S));
   }
   return slow;
 }

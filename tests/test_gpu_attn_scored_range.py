@@ -95,3 +95,43 @@ def test_infinite_scores(key, slope):
         tol = (S.U + 2 * E) * np.abs(Vh).max() + S.U * np.abs(want)
         assert np.all((np.abs(O - want) <= tol)[rows])
         assert np.all(np.abs(LSE[rows] - lse[rows]) <= E + 2.0 ** -22 * np.abs(lse[rows]))
+
+
+def _lse_bound(q, k, scale, z):
+    """Of one row's log of the sum: the products' sums, then 2^-20 of the scores
+    (the cap's arithmetic is relative to the score, not to the cap)."""
+    return 2.0 ** -17 * scale * (np.abs(k) @ np.abs(q)).max() + 2.0 ** -20 * np.abs(z).max() + 2.0 ** -18
+
+
+@pytest.mark.parametrize("cap", [1e3, 1e4, 1e6])
+def test_scores_far_below_the_cap(cap):
+    """Prompt and single token: what is lost of a small score does not grow
+    with the cap; nor beside scores that are near it."""
+    T = 150
+    rng = np.random.default_rng(7)
+    (Q, Qh), (K, Kh), (V, Vh) = (S.bf16(rng, 1, T, 128) for _ in range(3))
+    peak = 77                       # one query and one key whose product is about the cap
+    Q[0, peak], K[0, peak] = 0, 0
+    Q[0, peak, 0], K[0, peak, 0] = 1.0, 11.3 * cap
+    Q[0, :peak, 0] = 0
+    Q[0, peak + 1:, 0] = 0
+    Qh, Kh = Q.double().cpu().numpy(), K.double().cpu().numpy()
+    O, LSE = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+    tp.tp_attention_scored(Q, K, V, O, LSE, T, 1, 1, 1, 128, tp.score_params(softcap=cap, causal=True))
+    n = tp.tp_attention_decode_workspace_size(T, T, 1, 1, 1, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    cache = [x[:, None].expand(1, T, T, 128).contiguous() for x in (K, V)]
+    lengths = torch.arange(1, T + 1, dtype=torch.int32, device="cuda")
+    O1, LSE1 = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+    tp.tp_attention_decode(Q, None, None, *cache, lengths, O1, LSE1, ws, n, T, T, 1, 1, 1, 128,
+                           tp.score_params(softcap=cap))
+    tp.tp_sync_status()
+    for name, o, lse in (("prompt", O, LSE), ("token", O1, LSE1)):
+        o, lse = o[0].double().cpu().numpy(), lse[0, 0].double().cpu().numpy()
+        for i in range(T):
+            want, l = A.scored_row(Qh[0, i], Kh[0, :i + 1], Vh[0, :i + 1], 128 ** -0.5, cap)
+            z = cap * np.tanh(128 ** -0.5 * (Kh[0, :i + 1] @ Qh[0, i]) / cap)
+            E = _lse_bound(Qh[0, i], Kh[0, :i + 1], 128 ** -0.5, z)
+            assert abs(lse[i] - l) <= E + 2.0 ** -22 * abs(l), (name, i)
+            tol = (S.U + 2 * E) * np.abs(Vh).max() + S.U * np.abs(want)
+            assert np.all(np.abs(o[i] - want) <= tol), (name, i)
