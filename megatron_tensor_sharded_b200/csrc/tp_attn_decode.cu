@@ -650,7 +650,7 @@ tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a) {
   prm.s = score_consts(a.scale, a.cap);
   prm.err = c.err_word;
   prm.ctas = static_cast<int32_t>(decode_ctas(c.num_sms, a.B, a.capacity, a.p, a.hq, a.hkv));
-  const int cap = cap_form(prm.s.cap_log2);
+  const int cap = cap_form(prm.s);
   if (prm.rows == 8) {
     if (cap == kFineCap) return launch_form<kFineCap, 1>(c, prm);
     if (cap == kCoarseCap) return launch_form<kCoarseCap, 1>(c, prm);

@@ -1380,7 +1380,7 @@ tp_status launch_attention_scored_bwd(const LaunchCtx& c, const ScoreCall& a) {
   prm.wait.err = c.err_word;
   prm.wait.timeout_ns = c.timeout_ns;
   prm.debug_drop = c.debug_drop;
-  const int cap = cap_form(prm.s.cap_log2);
+  const int cap = cap_form(prm.s);
   if (cap == kFineCap) return launch_form<kFineCap>(c, prm, a, mQ, mK, mV, mdO);
   if (cap == kCoarseCap) return launch_form<kCoarseCap>(c, prm, a, mQ, mK, mV, mdO);
   return launch_form<kNoCap>(c, prm, a, mQ, mK, mV, mdO);

@@ -92,9 +92,9 @@ constexpr uint32_t O_COL0 = NS * BKV, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float kBoundLog2 = 80.0f;          // |z| in log2 that needs no running maximum
 
-// kCap: no bias, bounded; kCapAny: with a maximum; kCapFine: the same past kCoarseCapLog2
+// kCap: no bias, bounded; kCapAny: with a maximum; kCapFine: the same in the finer form
 enum { kPlain = 0, kBias = 1, kCap = 2, kCapAny = 3, kCapFine = 4 };
-static_assert(kBoundLog2 <= kCoarseCapLog2, "kCap takes the coarse form");
+static_assert(kCoarseCapLog2 <= kBoundLog2, "kCap: the caps of the coarse form need no maximum");
 
 struct ScoredParams {
   int32_t T, p, hq, hkv, group, q_blocks, num_units, causal;
@@ -816,11 +816,10 @@ tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a) {
   prm.wait.err = c.err_word;
   prm.wait.timeout_ns = c.timeout_ns;
   prm.debug_drop = c.debug_drop;
-  if (a.cap > 0.0f) {
-    if (a.slopes == nullptr && prm.s.cap_log2 <= kBoundLog2) return launch_mode<kCap>(c, prm, mQ, mK, mV);
-    if (cap_form(prm.s.cap_log2) == kFineCap) return launch_mode<kCapFine>(c, prm, mQ, mK, mV);
-    return launch_mode<kCapAny>(c, prm, mQ, mK, mV);
-  }
+  const int form = cap_form(prm.s);
+  if (form == kFineCap) return launch_mode<kCapFine>(c, prm, mQ, mK, mV);
+  if (form == kCoarseCap && a.slopes != nullptr) return launch_mode<kCapAny>(c, prm, mQ, mK, mV);
+  if (form == kCoarseCap) return launch_mode<kCap>(c, prm, mQ, mK, mV);
   if (a.slopes != nullptr) return launch_mode<kBias>(c, prm, mQ, mK, mV);
   return launch_mode<kPlain>(c, prm, mQ, mK, mV);
 }

@@ -51,16 +51,13 @@ constexpr double kTanh[4] = {0.999999463558197, -0.33326318860054016, 0.13190296
 // heads, queries of standard deviation 8, cap 50: 480 us, 597 with it).
 constexpr float kCoarseCapLog2 = 80.0f;
 enum { kNoCap = 0, kCoarseCap = 1, kFineCap = 2 };
-inline int cap_form(float cap_log2) {
-  return !(cap_log2 > 0.0f) ? kNoCap : cap_log2 <= kCoarseCapLog2 ? kCoarseCap : kFineCap;
-}
 
 // Scores z of a raw product s = q.k, in units of log2: z = log2(e) *
 // (cap tanh(scale s / cap) - slope |i - j|).
 struct ScoreConsts {
   float scale_log2;    // log2(e) scale
   float poly[4];       // z = s (p0 + u (p1 + u (p2 + u p3))), u = s^2, for |s| <= small
-  float small;         // scale |s| / cap <= 1/2
+  float small;         // scale |s| / cap <= 1/2; -1: a poly is not a normal number
   float two_x;         // 2 log2(e) scale / cap: tanh by e^(2x) beyond it
   float cap_log2;      // log2(e) cap (0: scores are not capped)
   float scale;         // scale itself (gradients)
@@ -75,11 +72,19 @@ inline ScoreConsts score_consts(float scale, float cap) {
     const double x = static_cast<double>(scale) / cap;
     for (int i = 0; i < 4; ++i) k.poly[i] = static_cast<float>(l2e * cap * kTanh[i] * std::pow(x, 2 * i + 1));
     k.small = static_cast<float>(0.5 / x);
+    // (scale/cap of 10^6 takes poly[3] past fp32 -- 0 times it is NaN --, a cap of
+    // 10^6 below it; scores then go through x_of_s one by one)
+    for (float c : k.poly)
+      if (!std::isnormal(c)) k.small = -1.0f;
     k.two_x = static_cast<float>(2.0 * l2e * x);
     k.cap_log2 = static_cast<float>(l2e * cap);
     k.x_of_s = static_cast<float>(x);
   }
   return k;
+}
+
+inline int cap_form(const ScoreConsts& k) {
+  return !(k.cap_log2 > 0.0f) ? kNoCap : k.cap_log2 <= kCoarseCapLog2 && k.small > 0.0f ? kCoarseCap : kFineCap;
 }
 
 struct ScoreCall {

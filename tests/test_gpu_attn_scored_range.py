@@ -135,3 +135,47 @@ def test_scores_far_below_the_cap(cap):
             assert abs(lse[i] - l) <= E + 2.0 ** -22 * abs(l), (name, i)
             tol = (S.U + 2 * E) * np.abs(Vh).max() + S.U * np.abs(want)
             assert np.all(np.abs(o[i] - want) <= tol), (name, i)
+
+
+@pytest.mark.parametrize("cap,ratio,size", [(50.0, 9.9e5, 0.0), (50.0, 9.9e5, 1e-4), (1.0, 9e5, 1e-3), (1e6, 9e5, 0.0),
+                                            (1e6, 1.1e-9, 6000.0), (1e-3, 1.1e-9, 6000.0), (1e-3, 9e5, 1e-4),
+                                            (30.0, 1e-8, 2000.0)])
+@pytest.mark.parametrize("slope", [0.0, 0.01])
+def test_scale_over_cap_at_the_ends_of_its_range(cap, ratio, size, slope):
+    """Rows of zeros and rows whose scores lie around the cap."""
+    T, scale = 140, cap * ratio
+    rng = np.random.default_rng(2)
+    (Q, Qh), (K, Kh) = (S.bf16(rng, 1, T, 128, std=size) for _ in range(2))
+    V, Vh = S.bf16(rng, 1, T, 128)
+    Q[0, 3], Qh[0, 3] = 0, 0
+    sl = torch.tensor([slope], device="cuda") if slope else None
+    O, LSE = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+    score = tp.score_params(scale=scale, softcap=cap, slopes=sl, causal=True)
+    scale = float(score.scale)          # as fp32
+    tp.tp_attention_scored(Q, K, V, O, LSE, T, 1, 1, 1, 128, score)
+    dO, _ = S.bf16(rng, 1, T, 128)
+    g = [torch.zeros_like(x) for x in (Q, K, V)]
+    n = tp.tp_attention_scored_backward_workspace_size(T, 1, 1, 1, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    tp.tp_attention_scored_backward(Q, K, V, O, LSE, dO, *g, ws, n, T, 1, 1, 1, 128, score)
+    n = tp.tp_attention_decode_workspace_size(T, T, 1, 1, 1, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    cache = [x[:, None].expand(1, T, T, 128).contiguous() for x in (K, V)]
+    O1, LSE1 = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+    tp.tp_attention_decode(Q, None, None, *cache, torch.arange(1, T + 1, dtype=torch.int32, device="cuda"), O1, LSE1,
+                           ws, n, T, T, 1, 1, 1, 128, score)
+    tp.tp_sync_status()
+    assert all(torch.isfinite(x).all() for x in g)
+    want, lse = A.scored_head(Qh[0], Kh[0], Vh[0], np.tri(T, dtype=bool), scale, cap, slope)
+    for name, o, l in (("prompt", O, LSE), ("token", O1, LSE1)):
+        o, l = o[0].double().cpu().numpy(), l[0, 0].double().cpu().numpy()
+        for i in range(T):
+            x = scale * (Kh[0, :i + 1] @ Qh[0, i])
+            z = cap * np.tanh(x / cap) - slope * np.arange(i, -1, -1)
+            # the products' rounding as far as the cap's derivative lets it through
+            mag = 2.0 ** -17 * scale * (np.abs(Kh[0, :i + 1]) @ np.abs(Qh[0, i]))
+            near = np.maximum(np.abs(x) - mag, 0)
+            E = (mag / np.cosh(np.minimum(near / cap, 300.0)) ** 2).max() + 2.0 ** -20 * np.abs(z).max() + 2.0 ** -18
+            assert abs(l[i] - lse[i]) <= E + 2.0 ** -22 * abs(lse[i]), (name, i)
+            tol = (S.U + 2 * E) * np.abs(Vh).max() + S.U * np.abs(want[i])
+            assert np.all(np.abs(o[i] - want[i]) <= tol), (name, i)
