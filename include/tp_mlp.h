@@ -662,6 +662,11 @@ size_t tp_attention_mask_size(int64_t T);
  * gives NaN (LSE +inf or NaN), one whose scores are all -inf 0 (LSE -inf).
  * Scores, maxima, sums and the accumulator are fp32; probabilities are rounded
  * to bf16 before P V and O once at the end.  The results are reproducible.
+ * Range of V: O is summed before it is divided, over exponentials of at most w =
+ * 2^8 beside their maximum's, or, where softcap is at most 55 without slopes, of
+ * exp(-softcap) to w = exp(softcap) (no maximum is taken).  max|V| w T has to stay
+ * below 2^128 (softcap 50, 4096 tokens: |V| < 2^43), and in the second form
+ * values below 2^-126 w lose digits where all scores lie near -softcap.
  */
 tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void* O, float* LSE,
                               int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,

@@ -179,3 +179,29 @@ def test_scale_over_cap_at_the_ends_of_its_range(cap, ratio, size, slope):
             assert abs(l[i] - lse[i]) <= E + 2.0 ** -22 * abs(lse[i]), (name, i)
             tol = (S.U + 2 * E) * np.abs(Vh).max() + S.U * np.abs(want[i])
             assert np.all(np.abs(o[i] - want[i]) <= tol), (name, i)
+
+
+@pytest.mark.parametrize("cap,slopes", [(50.0, 0.0), (55.0, 0.0), (50.0, 1e-3), (60.0, 0.0)])
+@pytest.mark.parametrize("side", [1.0, -1.0])
+def test_range_of_v(cap, slopes, side):
+    """Every score next to +-cap: V as large as the sums allow (within a factor
+    of four) and, at -cap, as small as keeps its digits."""
+    p, T, h = 1, 300, 1
+    rng = np.random.default_rng(3)
+    (Q, Qh), (K, Kh) = (S.bf16(rng, p, T, 128, std=0.01) for _ in range(2))
+    Q[..., 0], K[..., 0] = 64.0, side * 64.0        # scale q.k = +-362, tanh = 1 but for 2^-17
+    Qh, Kh = Q.double().cpu().numpy(), K.double().cpu().numpy()
+    log2w = cap / np.log(2) if cap <= 55 and not slopes else 8.0
+    for log2v in (np.floor(128 - log2w - np.log2(4 * T) - 2), np.ceil(-126 + log2w + 4)):
+        V, Vh = S.bf16(rng, p, T, 128)
+        V, Vh = V * 2.0 ** log2v, Vh * 2.0 ** log2v
+        sl = torch.tensor([slopes], device="cuda") if slopes else None
+        O, LSE = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+        tp.tp_attention_scored(Q, K, V, O, LSE, T, p, h, h, 128, tp.score_params(softcap=cap, slopes=sl, causal=True))
+        tp.tp_sync_status()
+        want, lse = A.scored_head(Qh[0], Kh[0], Vh[0], np.tri(T, dtype=bool), 128 ** -0.5, cap, slopes)
+        # (the cap leaves nothing of the products' rounding)
+        E = 2.0 ** -20 * cap + 2.0 ** -22 * slopes * T + 2.0 ** -18
+        vmax = np.maximum.accumulate(np.abs(Vh[0]).max(1))[:, None]
+        assert np.all(np.abs(O[0].double().cpu().numpy() - want) <= (S.U + 2 * E) * vmax + S.U * np.abs(want))
+        assert np.all(np.abs(LSE[0, 0].double().cpu().numpy() - lse) <= E + 2.0 ** -22 * np.abs(lse))
