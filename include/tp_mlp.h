@@ -685,8 +685,14 @@ tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void*
  *   workspace  tp_attention_scored_backward_workspace_size(...) bytes,
  *              256-byte aligned
  * P and dS are rounded to bf16 before their products, the gradients once at
- * the end; sums are fp32 in a fixed order (reproducible).  A row that sees one
- * key has exactly no gradient through its score.
+ * the end; sums are fp32 in a fixed order (reproducible).  D comes from O as it
+ * is given, i.e. as the forward call rounded it to bf16: dS_ij is off by up to
+ * P_ij 2^-8 sum_d |dO_id| (max_j |v_jd| + |O_id|) through it (O's probabilities and O
+ * are rounded by half a bf16 step, 2^-8, each), which does not shrink where
+ * dO_i.v_j - D_i itself is small, as in rows that see few keys or whose softmax
+ * has one large term (dQ and dK of packed documents: 0.0027 in the 2-norm, 0.0017
+ * with D from an fp32 O).  A row that sees one key has exactly no gradient
+ * through its score.
  */
 tp_status tp_attention_scored_backward(const void* Q, const void* K, const void* V, const void* O,
                                        const float* LSE, const void* dO, void* dQ, void* dK,

@@ -330,3 +330,45 @@ def test_long_runs_of_blocks_that_no_mask_cuts(case):
     _check(case, host, slopes, seen, inside, O, LSE, grads, kv_heads={(0, 0)})
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(grads, _call(case, dev, score, O, LSE)))
+
+
+@pytest.mark.parametrize("case", [
+    dict(p=1, T=300, h=4, hkv=2, off=list(range(0, 301, 2))), dict(p=1, T=300, h=4, hkv=2, off=list(range(0, 301, 3)), cap=30.0),
+    dict(p=1, T=290, h=2, hkv=2, off=list(range(0, 280, 7)) + [285], slopes=1.0),
+    dict(p=1, T=200, h=2, hkv=1, off=list(range(0, 201, 20)), causal=False, std=2.0)], ids=["twos", "threes", "sevens", "peaked"])
+def test_short_documents_against_the_true_gradient(case):
+    """Forward, then backward, element by element against the gradient from exact
+    O and LSE.  Beside the bound at the top, D is off by what O is:
+    sum_d |dO_d| ((u + 2E) max_j|v_jd| + u |O_d|) in every dS of the row, times P f."""
+    p, T, h, hkv = case["p"], case["T"], case["h"], case["hkv"]
+    dev, host, slopes, score, seen, inside, _, _ = _setup(case, seed=4)
+    O, LSE = torch.zeros_like(dev[0]), torch.zeros(p, h // p, T, device="cuda")
+    tp.tp_attention_scored(dev[0], dev[1], dev[2], O, LSE, T, p, h, hkv, 128, score)
+    got = [x[0].double().cpu().numpy() for x in _call(case, dev, score, O, LSE)]
+    Q, K, V, dO = host
+    scale, cap, u, group = S.case_scale(case), case.get("cap", 0.0), S.U, h // hkv
+    for n in range(hkv):
+        k, v = S.head(K, 0, n), S.head(V, 0, n)
+        vmax = np.where(seen[:, :, None], np.abs(v)[None], 0.0).max(1)
+        want, tol = [np.zeros((T, 128)) for _ in range(2)], [np.zeros((T, 128)) for _ in range(2)]
+        for j in range(n * group, n * group + group):
+            q, do, sl = S.head(Q, 0, j), S.head(dO, 0, j), slopes[j]
+            E = 2 * S.score_error(q, k, scale, cap, sl, T)
+            z, t = A.scores(q, k, scale, cap, sl)
+            o, lse = A.scored_head(q, k, v, seen, scale, cap, sl)
+            E += 2.0 ** -22 * np.abs(np.where(inside, lse, 0)).max()
+            P = np.where(seen, np.exp(np.where(seen, z - np.where(inside, lse, 0.0)[:, None], 0.0)), 0.0)
+            d = do @ v.T - (do * o).sum(1, keepdims=True)
+            mag = np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o)).sum(1, keepdims=True)
+            off = (np.abs(do) * ((u + E) * vmax + u * np.abs(o))).sum(1, keepdims=True)
+            f = 1.0 if t is None else 1 - t * t
+            rel = u + E + 2.0 ** -13
+            dS = P * d * f
+            err = P * f * (rel * np.abs(d) + 2.0 ** -17 * mag + (1 + rel) * off) + 2.0 ** -18 * P * np.abs(d)
+            dq, bound = scale * dS @ k, scale * err @ np.abs(k)
+            assert np.all((np.abs(got[0][:, j * 128:j * 128 + 128] - dq) <= bound + u * np.abs(dq))[inside]), ("dQ", j)
+            for x, y in zip(want + tol, (scale * dS.T @ q, P.T @ do, scale * err.T @ np.abs(q), rel * P.T @ np.abs(do))):
+                x += y
+        for name, a, w, b in (("dK", got[1], want[0], tol[0]), ("dV", got[2], want[1], tol[1])):
+            a = a[:, n * 128:n * 128 + 128]
+            assert np.all((np.abs(a - w) <= b + u * np.abs(w))[inside]), (name, n)
