@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   float acc[2][16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = 0.0f;
-  for (int32_t t0 = blockIdx.x * P.tok; t0 < P.T; t0 += gridDim.x * P.tok) {
+  for (uint32_t at = blockIdx.x * P.tok; at < static_cast<uint32_t>(P.T); at += gridDim.x * P.tok) {
+    const int32_t t0 = static_cast<int32_t>(at);   // (at itself may pass 2^31)
     const int32_t ntok = min(P.tok, P.T - t0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -525,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     float acc[kSlots][2];
 #pragma unroll
     for (int n = 0; n < kSlots; ++n) acc[n][0] = acc[n][1] = 0.0f;
-    for (int32_t t0 = blockIdx.x * P.tok; t0 < P.T; t0 += gridDim.x * P.tok) {
+    for (uint32_t at = blockIdx.x * P.tok; at < static_cast<uint32_t>(P.T); at += gridDim.x * P.tok) {
+      const int32_t t0 = static_cast<int32_t>(at);   // (at itself may pass 2^31)
       const int32_t ntok = min(P.tok, P.T - t0);
       __syncthreads();
       fill_angles(P, t0, ntok, cs, sn);

@@ -209,3 +209,35 @@ def test_captured_and_replayed_on_a_side_stream():
         torch.cuda.synchronize()
         want = A.head_norm(_heads(Q.double().cpu().numpy(), D)[1], None, EPS)
         assert np.allclose(_heads(Qo.double().cpu().numpy(), D)[1], want, atol=2e-5)
+
+
+def test_as_many_tokens_as_int32_counts():
+    """2^31 - 1 tokens of one head of two elements: forward and backward at the
+    first and the last tokens."""
+    T, D = 2 ** 31 - 1, 2
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 27 GB")
+    w = torch.tensor([1.5, -0.5], device="cuda")
+    x, dy = (torch.empty(T * D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    y = torch.zeros_like(x)
+    plan, freq = tp.rope_plan(rotary_dim=D, base=10000.0), A.rope_frequencies(D, 10000.0)
+    tp.tp_qk_norm_rope(x, None, w, None, None, y, None, T, 1, 1, 0, D, plan, EPS, tp.TP_BF16)
+    n = tp.tp_qk_norm_rope_backward_workspace_size(T, 1, 1, 0, D)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dx = torch.zeros_like(x)
+    tp.tp_qk_norm_rope_backward(x, None, w, None, None, dy, None, dx, None, None, None, ws, n, T, 1, 1, 0, D, plan,
+                                EPS, tp.TP_BF16)
+    tp.tp_sync_status()
+    for lo in (0, 2 ** 30 - 7, T - 5000):
+        at = slice(lo * D, (lo + 5000) * D)
+        xh, dyh = (t[at].double().cpu().numpy().reshape(-1, 1, D) for t in (x, dy))
+        pos, wh = np.arange(lo, lo + 5000), w.double().cpu().numpy()
+        normed = A.head_norm(xh, wh, EPS)
+        want = A.rope_rotate(normed, pos, freq)
+        tol = U["bf16"] * np.abs(want) + 2.0 ** -18 * _others(normed, D, "half")
+        assert np.all(np.abs(y[at].double().cpu().numpy().reshape(want.shape) - want) <= tol)
+        want, _ = A.head_norm_backward(xh, wh, A.rope_rotate(dyh, pos, freq, inverse=True), EPS)
+        rms = np.sqrt((xh * xh).mean(-1, keepdims=True) + EPS)
+        g, xhat = _others(dyh, D, "half") * np.abs(wh), np.abs(xh / rms)
+        tol = U["bf16"] * np.abs(want) + 2.0 ** -17 / rms * (g + xhat * (g * xhat).mean(-1, keepdims=True))
+        assert np.all(np.abs(dx[at].double().cpu().numpy().reshape(want.shape) - want) <= tol)
