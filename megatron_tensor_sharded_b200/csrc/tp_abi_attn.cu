@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 
 #include "tp_internal.h"
@@ -35,13 +36,13 @@ tp_status cuda_status(cudaError_t e, const char* what) {
   TP_FAIL(TP_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// A buffer of the call: `self` names the input that an output may share its
-// whole buffer with.
+// A buffer of the call: `self` names the input (and no other that happens to
+// lie there) that an output may share its whole buffer with.
 struct Buf {
   const char* name;
   const void* ptr;
   size_t bytes;
-  const void* self;
+  const char* self;
 };
 
 bool overlap(const Buf& a, const Buf& b) {
@@ -52,7 +53,7 @@ bool overlap(const Buf& a, const Buf& b) {
 tp_status check_overlaps(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
   for (auto o = outs.begin(); o != outs.end(); ++o) {
     for (const Buf& i : ins)
-      if (overlap(*o, i) && !(o->ptr == i.ptr && i.ptr == o->self))
+      if (overlap(*o, i) && !(o->ptr == i.ptr && o->self != nullptr && std::strcmp(o->self, i.name) == 0))
         TP_FAIL(TP_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
     for (auto q = o + 1; q != outs.end(); ++q)
       if (overlap(*o, *q)) TP_FAIL(TP_ERR_INVALID_ARG, "%s overlaps %s", o->name, q->name);
@@ -126,7 +127,7 @@ tp_status rope_impl(RopeCall a, int n_heads, int n_kv_heads, void* stream) {
   a.hk = a.K != nullptr ? n_kv_heads / a.p : 0;
   const size_t es = a.dtype == TP_BF16 ? 2 : 4, row = static_cast<size_t>(a.T) * a.dh * a.p * es;
   const size_t w = static_cast<size_t>(a.dh) * 4;
-  TP_TRY(check_overlaps({{"Q_out", a.Qo, row * a.hq, a.Q}, {"K_out", a.Ko, row * a.hk, a.K}},
+  TP_TRY(check_overlaps({{"Q_out", a.Qo, row * a.hq, "Q"}, {"K_out", a.Ko, row * a.hk, "K"}},
                         {{"Q", a.Q, row * a.hq, nullptr},
                          {"K", a.K, row * a.hk, nullptr},
                          {"wq", a.wq, w, nullptr},
@@ -366,8 +367,8 @@ tp_status tp_qk_norm_rope_backward(const void* Q, const void* K, const float* wq
     return TP_OK;
   }
   TP_TRY(check_workspace(workspace, workspace_bytes, need));
-  TP_TRY(check_overlaps({{"dQ", dQ, row * a.hq, dQ_out},
-                         {"dK", dK, row * a.hk, dK_out},
+  TP_TRY(check_overlaps({{"dQ", dQ, row * a.hq, "dQ_out"},
+                         {"dK", dK, row * a.hk, "dK_out"},
                          {"dwq", dwq, w, nullptr},
                          {"dwk", dwk, w, nullptr},
                          {"workspace", workspace, need, nullptr}},

@@ -121,3 +121,14 @@ def test_backward_refusals():
                        (dict(dwq=7 * A1 + 2), 3), (dict(dwk=7 * A1), 1), (dict(dQ=A1), 1),
                        (dict(dwq=9 * A1), 1), (dict(eps=-1.0), 1), (dict(n_heads=5), 2)):
         assert _bwd(**kw) == status, kw
+
+
+def test_an_output_in_place_of_two_inputs():
+    """In place is one input's buffer; where another input is read there too its
+    rows would be overwritten before they are read."""
+    for call in (_rope, _norm):
+        assert call(K=A1, Q_out=A1) == 1           # Q turned in place, K read from Q
+        assert call(K=A1, K_out=A1) == 1
+    assert _bwd(dK_out=A3, dQ=A3) == 1
+    assert _bwd(Q=A3, dQ=A3) == 1
+    assert _bwd(dK_out=A3, dK=A3) == 1
