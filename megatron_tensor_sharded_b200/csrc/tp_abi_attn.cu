@@ -270,7 +270,8 @@ tp_status tp_rope_plan_init(const tp_rope_config* cfg, tp_rope_plan* plan) {
       const real g = std::min(real(1), std::max(real(0), (i - lo) / span));
       w = w * (1 - g) + w / f * g;
     }
-    plan->turn[i] = static_cast<uint64_t>(std::ldexp(w / two_pi, 64));   // w <= 1: below 2^62
+    // to the nearest (w <= 1: below 2^62)
+    plan->turn[i] = static_cast<uint64_t>(std::floor(std::ldexp(w / two_pi, 64) + real(0.5)));
   }
   return TP_OK;
 }

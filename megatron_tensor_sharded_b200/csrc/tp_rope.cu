@@ -17,8 +17,9 @@
 //
 // Angles: the plan holds freq_i / 2 pi as a 64-bit fraction of a turn, so
 // t * turn_i mod 2^64 is the angle's fraction of a turn, exactly reduced by
-// the integer product's wrap-around (error t * 2^-65 turns): far positions
-// lose nothing, where t * freq_i in fp32 would be off by 0.03 rad at 10^6.
+// the integer product's wrap-around (error: t times the plan's, half a unit and
+// 2^-62 of the frequency, at most 1.2 * 2^-64 turns): far positions lose
+// nothing, where t * freq_i in fp32 would be off by 0.03 rad at 10^6.
 //
 // Two kernels of each: the vector one gives a thread 16 elements of a head
 // (two 8-element chunks whose pairs belong together; dh/16 lanes a head) and

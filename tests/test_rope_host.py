@@ -132,3 +132,16 @@ def test_an_output_in_place_of_two_inputs():
     assert _bwd(dK_out=A3, dQ=A3) == 1
     assert _bwd(Q=A3, dQ=A3) == 1
     assert _bwd(dK_out=A3, dK=A3) == 1
+
+
+@pytest.mark.parametrize("r,base", [(128, 500000.0), (64, 10000.0), (256, 1e6), (18, 77.0)])
+def test_plan_is_rounded_to_the_nearest(r, base):
+    """Against 60 decimal digits: half a unit, and 2^-62 of the frequency for the
+    power in long double."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    turn = tp.rope_plan(rotary_dim=r, base=base).turn
+    for i in range(r // 2):
+        want = Decimal(base) ** (Decimal(-2 * i) / Decimal(r)) / two_pi * 2 ** 64
+        assert abs(Decimal(turn[i]) - want) <= Decimal("0.5") + want / 2 ** 62, i
