@@ -742,8 +742,9 @@ size_t tp_attention_decode_workspace_size(int64_t B, int64_t capacity, int p, in
 /* Synchronise `stream`, then report (and clear) the device status word of
  * the current device: TP_ERR_DEVICE_TIMEOUT if a bounded wait ran out since
  * the last call, TP_ERR_INVALID_ARG if tp_attention_decode met a length that
- * its cache does not hold, TP_ERR_CUDA if the stream reported an error, else
- * TP_OK. */
+ * its cache does not hold, TP_ERR_CUDA if the stream reported an error or a
+ * kernel found its shared memory laid out otherwise than it needs and did
+ * nothing, else TP_OK. */
 tp_status tp_sync_status(void* stream);
 
 /* Limit for every bounded device-side wait, in nanoseconds (default 2e9).

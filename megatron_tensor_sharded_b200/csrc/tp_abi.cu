@@ -908,6 +908,8 @@ tp_status tp_sync_status(void* stream) {
     if (e != cudaSuccess) return fail(TP_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
     if (word == kErrLength)
       return fail(TP_ERR_INVALID_ARG, "a sequence's length exceeds its cache");
+    if ((word & ~kErrLength) == kErrSmem)
+      return fail(TP_ERR_CUDA, "a kernel's shared memory does not start at a multiple of 1024 bytes");
     return fail(TP_ERR_DEVICE_TIMEOUT, "device wait gave up (status bits 0x%x)", word);
   }
   return TP_OK;
