@@ -93,3 +93,18 @@ def test_nothing_to_do():
     assert tp.tp_kernel_launch_count() == n0
     assert tp.tp_attention_scored_backward_workspace_size(0, 1, 1, 1, 128) > 0
     assert tp.tp_attention_scored_backward_workspace_size(10, 1, 1, 1, 64) == 0
+
+
+@pytest.mark.parametrize("raw,device,agrees", [(lambda d: 70 + d, lambda: 1, True), (lambda d: 5, lambda: 1, False),
+                                               (lambda: 71, lambda: 1, False), (None, lambda: 1, False)])
+def test_the_short_way_to_the_current_stream_has_to_agree(monkeypatch, raw, device, agrees):
+    import torch
+    public = type("S", (), {"cuda_stream": 71})
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: public)
+    for name, f in (("_cuda_getCurrentRawStream", raw), ("_cuda_getDevice", device)):
+        if f is None:
+            monkeypatch.delattr(torch._C, name, raising=False)
+        else:
+            monkeypatch.setattr(torch._C, name, f, raising=False)
+    way = tp._find_raw_stream()
+    assert way() == 71 and (way.__name__ == "short") == agrees
