@@ -165,6 +165,8 @@ tp_status score_call(ScoreCall* a, int64_t T, int p, int n_heads, int n_kv_heads
       TP_FAIL(TP_ERR_INVALID_ARG, "scale must be > 0 (or 0 for 1/sqrt(head_dim))");
     a->scale = s->scale;
   }
+  if (!std::isfinite(score_consts(a->scale, 0.0f).scale_log2))
+    TP_FAIL(TP_ERR_UNSUPPORTED, "scale %g (up to 2.3e38 is provided)", a->scale);
   if (!(s->softcap >= 0.0f) || !std::isfinite(s->softcap))
     TP_FAIL(TP_ERR_INVALID_ARG, "softcap must be >= 0");
   if (s->softcap > 0.0f && (s->softcap < 1e-3f || s->softcap > 1e6f ||
@@ -189,6 +191,18 @@ size_t score_bwd_ws(ScoreCall a) {
   return score_delta_ws(a) + score_bad_ws(a) + align256(score_dkv_bytes(a));
 }
 
+// Heads and options of a backward call into `a`: a CTA counts the steps of dK
+// and dV that are its share in 32 bits.
+tp_status score_bwd_call(ScoreCall* a, int64_t T, int p, int n_heads, int n_kv_heads, int head_dim,
+                         const tp_score_params* s) {
+  TP_TRY(score_call(a, T, p, n_heads, n_kv_heads, head_dim, s));
+  const double tiles = static_cast<double>(ceil_div(T, kAttnTile));
+  const double seen = a->causal && a->mask == nullptr ? (tiles + 1) / 2 : tiles;
+  if (n_heads * tiles * (seen + kUnitCost) / kScoreDkvCtas >= 0x1p31)
+    TP_FAIL(TP_ERR_UNSUPPORTED, "sizes too large (T = %lld, %d heads)", (long long)T, n_heads);
+  return TP_OK;
+}
+
 // Sizes and options of a decode call into `a` (its T is the batch).
 tp_status decode_sizes(ScoreCall* a, int64_t B, int64_t capacity, int p, int n_heads,
                        int n_kv_heads, int head_dim, const tp_score_params* s) {
@@ -199,6 +213,11 @@ tp_status decode_sizes(ScoreCall* a, int64_t B, int64_t capacity, int p, int n_h
   if (capacity > (int64_t(1) << 30) || B > (1 << 20) || B * n_heads > (int64_t(1) << 30) ||
       B * n_kv_heads * capacity > (int64_t(1) << 44))
     TP_FAIL(TP_ERR_UNSUPPORTED, "sizes too large (B = %lld, capacity = %lld)", (long long)B,
+            (long long)capacity);
+  // a CTA finds its place among all sequences' tiles of a head in 32 bits
+  const int64_t tiles = capacity / kDecodeTile + 1;
+  if (tiles * a->p * decode_items(a->hq, a->hkv) > (int64_t(1) << 31))
+    TP_FAIL(TP_ERR_UNSUPPORTED, "sizes too large (%d / %d heads, capacity = %lld)", n_heads, n_kv_heads,
             (long long)capacity);
   return TP_OK;
 }
@@ -449,7 +468,9 @@ tp_status tp_attention_scored(const void* Q, const void* K, const void* V, void*
 size_t tp_attention_scored_backward_workspace_size(int64_t T, int p, int n_heads, int n_kv_heads,
                                                    int head_dim) {
   ScoreCall a{};
-  if (score_call(&a, T, p, n_heads, n_kv_heads, head_dim, nullptr) != TP_OK) return 0;
+  tp_score_params least{};   // (the mask that leaves the fewest steps)
+  least.causal = 1;
+  if (score_bwd_call(&a, T, p, n_heads, n_kv_heads, head_dim, &least) != TP_OK) return 0;
   return T == 0 ? 256 : score_bwd_ws(a);
 }
 
@@ -460,7 +481,7 @@ tp_status tp_attention_scored_backward(const void* Q, const void* K, const void*
                                        const tp_score_params* score, void* stream) {
   set_error_detail("%s", "");
   ScoreCall a{};
-  TP_TRY(score_call(&a, T, p, n_heads, n_kv_heads, head_dim, score));
+  TP_TRY(score_bwd_call(&a, T, p, n_heads, n_kv_heads, head_dim, score));
   if (T == 0) return TP_OK;
   TP_TRY(check_bf16(Q, "Q"));
   TP_TRY(check_bf16(K, "K"));

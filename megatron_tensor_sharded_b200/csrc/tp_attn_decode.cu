@@ -42,7 +42,7 @@ namespace tpk {
 namespace {
 
 constexpr int DH = 128;
-constexpr int TILE = 64;                 // keys of a tile, 16 a warp
+constexpr int TILE = kDecodeTile;        // keys of a tile, 16 a warp
 constexpr int WARPS = 4;
 constexpr int NST = 3;                   // ring slots of a warp
 constexpr int MROWS = 16;                // most query heads of an item
@@ -610,14 +610,10 @@ tp_status launch_form(const LaunchCtx& c, const DecodeParams& prm) {
 
 }  // namespace
 
-// Query heads of an item: 8 where one column tile holds the group.
-int item_rows(int group) { return group <= 8 ? 8 : MROWS; }
-
 // CTAs that share the line of tiles: two an SM, fewer where the caches could
 // not give each a tile.
 int64_t decode_ctas(int num_sms, int64_t B, int64_t capacity, int p, int hq, int hkv) {
-  const int64_t mtiles = (hq / hkv + item_rows(hq / hkv) - 1) / item_rows(hq / hkv);
-  const int64_t most = B * p * hkv * mtiles * ((capacity + TILE - 1) / TILE);
+  const int64_t most = B * p * decode_items(hq, hkv) * ((capacity + TILE - 1) / TILE);
   int64_t full = static_cast<int64_t>(num_sms) * CTAS_PER_SM;
   if (full > kMaxDecodeCtas) full = kMaxDecodeCtas;
   return most < full ? most : full;
@@ -643,9 +639,9 @@ tp_status launch_attention_decode(const LaunchCtx& c, const DecodeCall& a) {
   prm.hq = a.hq;
   prm.hkv = a.hkv;
   prm.group = a.hq / a.hkv;
-  prm.rows = item_rows(prm.group);
+  prm.rows = decode_rows(prm.group);
   prm.mtiles = (prm.group + prm.rows - 1) / prm.rows;
-  prm.heads = a.p * a.hkv * prm.mtiles;
+  prm.heads = static_cast<int32_t>(a.p * decode_items(a.hq, a.hkv));
   prm.capacity = a.capacity;
   prm.s = score_consts(a.scale, a.cap);
   prm.err = c.err_word;

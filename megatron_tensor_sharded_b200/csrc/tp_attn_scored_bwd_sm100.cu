@@ -84,10 +84,6 @@ constexpr uint32_t IDESC_KN = idesc_bf16_f32(BT, DH, 0, 1);   // A in TMEM, B ro
 template <int CAP>
 constexpr int kPolyPairs = CAP ? 0 : 2;
 constexpr float kLog2e = 1.4426950408889634f;
-// A dkv unit's loads, start and stores, in steps (1999 tokens of five documents,
-// 64/8 heads, whole backward: 2 230 us, 4 226, 6 226, 8 228; a smaller one 49,
-// 42, 41, 41).
-constexpr int kUnitCost = 4;
 constexpr int kWholeUnits = 6;                // units a CTA from which none is cut
 constexpr int kCut = 1, kFirst = 2, kLast = 4, kEnd = 8;   // a step: cut by a mask; its unit's; the share's last
 constexpr int PART_FLOATS = 2 * BT * DH;      // dV and dK of a key tile

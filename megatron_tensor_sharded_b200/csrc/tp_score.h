@@ -115,6 +115,14 @@ struct DecodeCall {
   const float* slopes;
 };
 constexpr int kMaxDecodeCtas = 512;
+constexpr int kDecodeTile = 64;   // keys
+// Query heads of an item: 8 where one column tile holds the group, else 16; and
+// the items of a sequence in a shard.
+inline int decode_rows(int group) { return group <= 8 ? 8 : 16; }
+inline int64_t decode_items(int hq, int hkv) {
+  const int rows = decode_rows(hq / hkv);
+  return static_cast<int64_t>(hkv) * ((hq / hkv + rows - 1) / rows);
+}
 // CTAs of a decode call, and the bytes of their partials.
 int64_t decode_ctas(int num_sms, int64_t B, int64_t capacity, int p, int hq, int hkv);
 size_t decode_part_bytes(int64_t ctas);
@@ -125,6 +133,10 @@ cudaError_t launch_attention_mask(const LaunchCtx& c, const int32_t* off, int n_
 // Scratch of the backward's dK and dV for the call's sizes; kScoreDkvCtas: the
 // SMs of a B200.
 constexpr int kScoreDkvCtas = 148;
+// A dkv unit's loads, start and stores, in steps (1999 tokens of five documents,
+// 64/8 heads, whole backward: 2 230 us, 4 226, 6 226, 8 228; a smaller one 49,
+// 42, 41, 41).
+constexpr int kUnitCost = 4;
 int64_t score_dkv_ctas(const ScoreCall& a);
 size_t score_dkv_bytes(const ScoreCall& a);
 tp_status launch_attention_scored(const LaunchCtx& c, const ScoreCall& a);

@@ -108,3 +108,27 @@ def test_the_short_way_to_the_current_stream_has_to_agree(monkeypatch, raw, devi
             monkeypatch.setattr(torch._C, name, f, raising=False)
     way = tp._find_raw_stream()
     assert way() == 71 and (way.__name__ == "short") == agrees
+
+
+def test_sizes_past_what_a_block_counts():
+    """Shares of steps, places among tiles and scores that would leave 32 bits."""
+    huge = tp.score_params(scale=3e38)
+    a = dict(Q=B[0], K=B[1], V=B[2], O=B[3], LSE=B[4], T=300, p=1, n_heads=1, n_kv_heads=1, head_dim=128, score=huge,
+             stream=0, check=False)
+    assert tp.tp_attention_scored(**a) == 4
+    b = dict(a, dO=B[5], dQ=B[6], dK=B[7], dV=B[8], workspace=B[10], workspace_bytes=1 << 40)
+    assert tp.tp_attention_scored_backward(**b) == 4
+    # the steps of dK and dV: T^2 / 2^14 a head, shared by 148
+    size = tp.tp_attention_scored_backward_workspace_size
+    assert tp.tp_attention_scored_backward(**dict(b, T=2 ** 27, score=None)) == 4
+    assert tp.tp_attention_scored_backward(**dict(b, T=2 ** 30, score=tp.score_params(causal=True))) == 4
+    assert size(2 ** 26, 1, 1, 1, 128) > 0 and size(2 ** 30, 1, 1, 1, 128) == 0
+    # a sequence's tiles of all its heads
+    size = tp.tp_attention_decode_workspace_size
+    assert size(1, 2 ** 30, 1, 64, 64, 128) > 0 and size(1, 2 ** 30, 1, 1024, 1024, 128) == 0
+    assert size(1, 2 ** 30, 1, 1024, 64, 128) > 0
+    c = dict(Q=B[0], K_new=None, V_new=None, K_cache=B[1], V_cache=B[1] << 13, lengths=B[2], O=B[3], LSE=None,
+             workspace=B[4], workspace_bytes=1 << 30, B=1, capacity=2 ** 30, p=1, n_heads=1024, n_kv_heads=1024,
+             head_dim=128, stream=0, check=False)
+    assert tp.tp_attention_decode(**c) == 4
+    assert tp.tp_attention_decode(**dict(c, capacity=64, n_heads=1, n_kv_heads=1, score=huge)) == 4
