@@ -578,7 +578,8 @@ tp_status tp_rope(const void* Q, const void* K, const int32_t* positions, void* 
 
 /*
  * Norm of every query and key head with the rotation in the same pass:
- *   y = rotate(x * rstd * w),  rstd = (mean(x^2) + eps)^(-1/2) over the head.
+ *   y = rotate(x * rstd * w),  rstd = (mean(x^2) + eps)^(-1/2) over the head
+ * (the sum of squares in fp32: its root has to stay below 2^64).
  *   wq, wk  [head_dim] fp32, shared by all heads and shards; NULL: no weight
  *   plan    NULL: the norm alone
  *   eps     > 0
@@ -659,7 +660,9 @@ size_t tp_attention_mask_size(int64_t T);
  *   score  NULL: no options (every row sees every key)
  * A key adds nothing to a row that does not see it, whatever K and V hold
  * there (infinities and NaN too).  A row that sees a score of +inf or NaN
- * gives NaN (LSE +inf or NaN), one whose scores are all -inf 0 (LSE -inf).
+ * gives NaN (LSE +inf or NaN), one whose scores are all -inf 0 (LSE -inf), and
+ * one that sees a value of +-inf or NaN is not finite in that column and may
+ * be NaN in the others.
  * Scores, maxima, sums and the accumulator are fp32; probabilities are rounded
  * to bf16 before P V and O once at the end.  The results are reproducible.
  * Range of V: O is summed before it is divided, over exponentials of at most w =
