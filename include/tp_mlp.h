@@ -659,10 +659,11 @@ size_t tp_attention_mask_size(int64_t T);
  *   LSE    [p][n_heads/p][T] fp32 or NULL (the backward call needs it)
  *   score  NULL: no options (every row sees every key)
  * A key adds nothing to a row that does not see it, whatever K and V hold
- * there (infinities and NaN too).  A row that sees a score of +inf or NaN
- * gives NaN (LSE +inf or NaN), one whose scores are all -inf 0 (LSE -inf), and
- * one that sees a value of +-inf or NaN is not finite in that column and may
- * be NaN in the others.
+ * there (infinities and NaN too; with a softcap it may have a say in which of
+ * two forms of tanh the rows beside it take, 2^-21 softcap apart).  A row that
+ * sees a score of +inf or NaN gives NaN (LSE +inf or NaN), one whose scores are
+ * all -inf 0 (LSE -inf), and one that sees a value of +-inf or NaN is not
+ * finite in that column and may be NaN in the others.
  * Scores, maxima, sums and the accumulator are fp32; probabilities are rounded
  * to bf16 before P V and O once at the end.  The results are reproducible.
  * Range of V: O is summed before it is divided, over exponentials of at most w =

@@ -42,7 +42,8 @@
 //
 // Masks, and rows that hold infinities or NaN outside what is seen, as in the
 // forward kernel; here rows of Q and dO (dkv) and of K (dq) that the first kernel
-// marked are set to 0 in tiles that a mask cuts.
+// marked are set to 0 in tiles that a mask cuts, and what does see one is made
+// NaN (through `hit`, through dS).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -137,13 +138,16 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 }
 
 // 32 raw products -> P as bf16 pairs in pk and w = P (1 - tanh^2).  nl(e):
-// -LSE log2 e of columns e .. e + 3; seen(e): whether the pair counts.
-template <int CAP, bool BIAS, typename NegLse, typename Seen>
+// -LSE log2 e of columns e .. e + 3; seen: the columns that count where a mask
+// cuts the tile, sure: those of them whose row of the other operand is finite
+// (its rows that are not are set to 0 while the scores are formed, so whether
+// they are NaN here is a matter of time: they must not choose the cap's form).
+template <int CAP, bool BIAS, typename NegLse>
 __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], uint32_t (&pk)[16],
                                            const BwdParams& P, float slope2, float dist0, int side,
-                                           bool cut, NegLse nl, Seen seen) {
+                                           bool cut, uint32_t seen, uint32_t sure, NegLse nl) {
   if (CAP) {
-    cap_chunk<CAP == kFineCap>(v, P.s);
+    cap_chunk<CAP == kFineCap, true>(v, P.s, cut, sure);
     const uint64_t ic = f2_pack(P.neg_inv_cap2, P.neg_inv_cap2), one = f2_pack(1.0f, 1.0f);
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -174,7 +178,7 @@ __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], ui
   if (cut) {   // (the cap's derivative of what is not seen may be NaN)
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      if (!seen(e)) {
+      if (!((seen >> e) & 1u)) {
         v[e] = 0;
         if (CAP) w[e] = 0.0f;
       }
@@ -193,9 +197,9 @@ __device__ __forceinline__ void prob_chunk(uint32_t (&v)[32], float (&w)[32], ui
 }
 
 // 32 products dP -> dS = w (dP - D) as bf16 pairs; nd(e): -D of columns e .. e + 3.
-template <typename NegDelta, typename Seen>
-__device__ __forceinline__ void grad_chunk(uint32_t (&v)[32], const float (&w)[32],
-                                           uint32_t (&pk)[16], bool cut, NegDelta nd, Seen seen) {
+template <typename NegDelta>
+__device__ __forceinline__ void grad_chunk(uint32_t (&v)[32], const float (&w)[32], uint32_t (&pk)[16],
+                                           bool cut, uint32_t seen, NegDelta nd) {
   uint64_t n[2];
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
@@ -209,7 +213,7 @@ __device__ __forceinline__ void grad_chunk(uint32_t (&v)[32], const float (&w)[3
   if (cut) {   // 0 * NaN from what is not seen
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      if (!seen(e)) v[e] = 0;
+      if (!((seen >> e) & 1u)) v[e] = 0;
   }
 #pragma unroll
   for (int e = 0; e < 32; e += 2)
@@ -819,18 +823,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const float dist0 = static_cast<float>(q0 - key);
       const int32_t kb = key / BT;
       const int side = step.x > kb ? 1 : step.x < kb ? -1 : 0;
-      uint32_t seen = 0xffffffffu;   // columns that see this key
+      uint32_t seen = 0xffffffffu, odd = 0;   // columns that see this key; that are not finite
       if (cut) {
-        const int32_t lo = min(max(by.x - q0, 0), 32), hi = min(max(by.y - q0, 0), 32);
-        seen = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
-        if (seen & bad[(n % NB) * 4 + part]) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
+        seen = columns_in(by.x - q0, by.y - q0);
+        odd = seen & bad[(n % NB) * 4 + part];
+        if (odd != 0) atomicOr(&hit[(nu % 3) * 4 + quad], 1u << lane);
       }
-      auto sees = [&](int e) { return ((seen >> e) & 1u) != 0; };
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(s_free);
-      prob_chunk<CAP, BIAS>(v, w, pk, P, __int_as_float(step.z), dist0, side, cut,
-                            [&](int e, uint64_t& a, uint64_t& b) { lds4(vl + e * 4, a, b); }, sees);
+      prob_chunk<CAP, BIAS>(v, w, pk, P, __int_as_float(step.z), dist0, side, cut, seen, seen & ~odd,
+                            [&](int e, uint64_t& a, uint64_t& b) { lds4(vl + e * 4, a, b); });
       const uint32_t one = cut ? lone[(n % NB) * 4 + part] : 0u;
       if (one != 0) {
 #pragma unroll
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tmem_ld_wait();
       // P^T and dS^T over this quarter's own dP^T
       tmem_st_32x32b_x16(tdP + off, pk);
-      grad_chunk(v, w, pk, cut, [&](int e, uint64_t& a, uint64_t& b) { lds4(vd + e * 4, a, b); }, sees);
+      grad_chunk(v, w, pk, cut, seen, [&](int e, uint64_t& a, uint64_t& b) { lds4(vd + e * 4, a, b); });
       tmem_st_32x32b_x16(tdP + off + 16, pk);
       tmem_st_wait();
       tc_fence_before();
@@ -981,6 +984,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain = smem_u32(&bars[20 + NA]);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (21 + NA));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* const bad = tmem_slot + 2;   // [NA][4]: keys of a cut block that are not finite
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -1165,14 +1169,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (cut) {
+            uint32_t w[2] = {0u, 0u};
             if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {
                 const int row = h * 64 + (warp - 2) * 32 + lane;
-                if (row_not_finite(sK(n), row)) zero_row(sK(n), row);
+                const bool is_bad = row_not_finite(sK(n), row);
+                if (is_bad) zero_row(sK(n), row);
+                w[h] = __ballot_sync(0xffffffffu, is_bad);
               }
               fence_proxy_async_smem();
             }
+            if (lane == 0) {
+              bad[(n % NA) * 4 + (warp - 2)] = w[0];
+              bad[(n % NA) * 4 + 2 + (warp - 2)] = w[1];
+            }
+            __syncwarp();
             mbar_arrive(k_seen(looked));
             ++looked;
           }
@@ -1221,11 +1233,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int side = j * BT + BT - 1 <= q0 ? -1 : j * BT >= q0 + BT - 1 ? 1 : 0;
         float w[32];
         uint32_t v[32], pk[16];
-        auto sees = [&](int e) { return e >= rl && e < rh; };
+        const uint32_t seen = cut ? columns_in(rl, rh) : 0xffffffffu, odd = cut ? bad[(n % NA) * 4 + part] : 0u;
         tmem_ld_32x32b_x32(tS, v);
         tmem_ld_wait();
         // (P itself is not stored: dQ needs dS alone)
-        prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut, [&](int, uint64_t& a, uint64_t& b) { a = b = nlse; }, sees);
+        prob_chunk<CAP, BIAS>(v, w, pk, P, slope2, dist0, side, cut, seen, seen & ~odd,
+                              [&](int, uint64_t& a, uint64_t& b) { a = b = nlse; });
+        if (odd & seen) {   // (its row of K is 0 now: the NaN goes through dS)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((odd & seen) >> e & 1u) w[e] = NAN;
+        }
         if (cut && span.y - span.x == 1) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) w[e] *= 0.0f;
@@ -1238,7 +1256,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(dp_free);
-        grad_chunk(v, w, pk, cut, [&](int, uint64_t& a, uint64_t& b) { a = b = ndl; }, sees);
+        grad_chunk(v, w, pk, cut, seen, [&](int, uint64_t& a, uint64_t& b) { a = b = ndl; });
         tmem_st_32x32b_x16(tS, pk);
         tmem_st_wait();
         tc_fence_before();

@@ -212,13 +212,14 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint64_t sc2,
 // maximum that would carry it).
 template <int MODE>
 __device__ __forceinline__ void score_chunk(uint32_t (&v)[32], const ScoreConsts& S, float slope2,
-                                            float dist0, int side, bool whole, int32_t rl,
-                                            int32_t rh, bool& lost) {
+                                            float dist0, int side, bool whole, uint32_t seen,
+                                            bool& lost) {
   bool slow = false;
-  if (MODE >= kCap) slow = cap_chunk<MODE == kCapFine>(v, S);
+  if (MODE >= kCap)
+    slow = cap_chunk<MODE == kCapFine, false>(v, S, !whole, seen);
   if (MODE == kBias || MODE >= kCapAny)
     bias_chunk<MODE == kBias>(v, S.scale_log2, slope2, dist0, side);
-  if (!whole) mask_chunk(v, rl, rh);
+  if (!whole) mask_chunk(v, seen);
   if (MODE == kCap && slow) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) lost |= __uint_as_float(v[e]) != __uint_as_float(v[e]);
@@ -554,7 +555,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           break;
         }
         tc_fence_after();
-        const int32_t rl = seen.x - key0, rh = seen.y - key0;
+        auto columns = [&](int c) {   // that the row sees, of a chunk of a cut block
+          return columns_in(seen.x - key0 - c * 32, seen.y - key0 - c * 32);
+        };
         float dist0 = 0.0f;
         int side = 0;
         if (MODE == kBias || MODE >= kCapAny) {
@@ -570,8 +573,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t v[32];
             tmem_ld_32x32b_x32(tS + c * 32, v);
             tmem_ld_wait();
-            score_chunk<MODE>(v, S, slope2, dist0 + c * 32.0f, side, whole, rl - c * 32,
-                              rh - c * 32, lost);
+            score_chunk<MODE>(v, S, slope2, dist0 + c * 32.0f, side, whole, columns(c), lost);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               acc[0] = max3_nan(acc[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
@@ -631,10 +633,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t v[32], pk[16];
           tmem_ld_32x32b_x32(tS + c * 32, v);
           tmem_ld_wait();
-          if (MODE == kPlain && !whole) mask_chunk(v, rl - c * 32, rh - c * 32);
+          if (MODE == kPlain && !whole) mask_chunk(v, columns(c));
           if (MODE == kCap || MODE == kBias)
-            score_chunk<MODE>(v, S, slope2, dist0 + c * 32.0f, side, whole, rl - c * 32,
-                              rh - c * 32, lost);
+            score_chunk<MODE>(v, S, slope2, dist0 + c * 32.0f, side, whole, columns(c), lost);
           exp_chunk<kPolyPairs<MODE>, HAS_MAX>(v, f2_pack(scale, scale), f2_pack(off, off), sum2, pk);
           tmem_st_32x32b_x16(tS + c * 16, pk);
         }
@@ -645,10 +646,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           const volatile uint32_t* b = bad + slot * 4 + half * 2;
-          if (b[0] | b[1]) {
-            for (int e = 0; e < 64; ++e)
-              poison |= e >= rl && e < rh && ((b[e >> 5] >> (e & 31)) & 1);
-          }
+          const uint32_t b0 = b[0], b1 = b[1];
+          if (b0 | b1) poison |= ((b0 & columns(0)) | (b1 & columns(1))) != 0;
         }
         tc_fence_before();
         mbar_arrive(p_full(slot));

@@ -98,35 +98,62 @@ __device__ __forceinline__ float cap_score(float s, const ScoreConsts& S) {
   return S.cap_log2 * (fabsf(x) <= 0.5f ? near : far);
 }
 
-// 32 raw products -> capped scores in log2 units.  True where the warp took
-// the form of cap_score (some row's |scale s| > cap/2, or a NaN).
-template <bool FINE>
-__device__ __forceinline__ bool cap_chunk(uint32_t* v, const ScoreConsts& S) {
+// Whether all of the warp's 32 products a row are small against the cap.
+__device__ __forceinline__ bool all_small(const uint32_t* v, const ScoreConsts& S) {
   float mx[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
     mx[0] = max3_nan(mx[0], fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
     mx[1] = max3_nan(mx[1], fabsf(__uint_as_float(v[e + 2])), fabsf(__uint_as_float(v[e + 3])));
   }
-  const bool slow = !__all_sync(0xffffffffu, max3_nan(mx[0], mx[1], mx[1]) <= S.small);
-  if (!slow) {
-    const uint64_t c0 = f2_pack(S.poly[0], S.poly[0]), c1 = f2_pack(S.poly[1], S.poly[1]);
-    const uint64_t c2 = f2_pack(S.poly[2], S.poly[2]), c3 = f2_pack(S.poly[3], S.poly[3]);
+  return __all_sync(0xffffffffu, max3_nan(mx[0], mx[1], mx[1]) <= S.small) != 0;
+}
+
+__device__ __forceinline__ void cap_small(uint32_t (&v)[32], const ScoreConsts& S) {
+  const uint64_t c0 = f2_pack(S.poly[0], S.poly[0]), c1 = f2_pack(S.poly[1], S.poly[1]);
+  const uint64_t c2 = f2_pack(S.poly[2], S.poly[2]), c3 = f2_pack(S.poly[3], S.poly[3]);
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const uint64_t s = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-      const uint64_t u = f2_mul(s, s);
-      const uint64_t z = f2_mul(s, f2_fma(u, f2_fma(u, f2_fma(u, c3, c2), c1), c0));
-      float a, b;
-      f2_unpack(z, a, b);
-      v[e] = __float_as_uint(a);
-      v[e + 1] = __float_as_uint(b);
-    }
+  for (int e = 0; e < 32; e += 2) {
+    const uint64_t s = f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    const uint64_t u = f2_mul(s, s);
+    const uint64_t z = f2_mul(s, f2_fma(u, f2_fma(u, f2_fma(u, c3, c2), c1), c0));
+    float a, b;
+    f2_unpack(z, a, b);
+    v[e] = __float_as_uint(a);
+    v[e + 1] = __float_as_uint(b);
+  }
+}
+
+// 32 raw products -> capped scores in log2 units.  True where the warp took
+// the form of cap_score (some row's |scale s| > cap/2, or a NaN).  Columns that a
+// mask hides have a say in that too; the two forms agree to cap_score's accuracy.
+// HIDE, for a caller in whose cut tiles another warp sets rows that are not
+// finite to 0 meanwhile, so that their products are a matter of time: where one
+// is large, columns that are not in `sure` are set to 0 and it is asked again.
+// (In the forward, which has no such rows, that cost 355 -> 361 us.)
+template <bool FINE, bool HIDE>
+__device__ __forceinline__ bool cap_chunk(uint32_t (&v)[32], const ScoreConsts& S, bool cut, uint32_t sure) {
+  bool slow = !all_small(v, S);
+  if (HIDE && slow && cut) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((sure >> e) & 1u)) v[e] = 0;
+    slow = !all_small(v, S);
+  }
+  if (!slow) {
+    cap_small(v, S);
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(cap_score<FINE>(__uint_as_float(v[e]), S));
   }
   return slow;
+}
+
+// Columns [lo, hi) of 32 as bits.
+__device__ __forceinline__ uint32_t columns_in(int32_t lo, int32_t hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  return hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
 }
 
 // Scores -> scores - slope2 |dist0 + e|, all in log2 units; SCALE: v holds raw
@@ -163,11 +190,11 @@ __device__ __forceinline__ void bias_chunk(uint32_t* v, float scale, float slope
   }
 }
 
-// Columns outside [rl, rh) of a 32-column chunk become -inf.
-__device__ __forceinline__ void mask_chunk(uint32_t* v, int32_t rl, int32_t rh) {
+// Columns of a 32-column chunk that are not in `seen` become -inf.
+__device__ __forceinline__ void mask_chunk(uint32_t (&v)[32], uint32_t seen) {
 #pragma unroll
   for (int e = 0; e < 32; ++e)
-    if (e < rl || e >= rh) v[e] = 0xff800000u;
+    if (!((seen >> e) & 1u)) v[e] = 0xff800000u;
 }
 
 // Whether row `row` (0..127) of a 128 x 128 bf16 tile in shared memory (two

@@ -205,3 +205,71 @@ def test_range_of_v(cap, slopes, side):
         vmax = np.maximum.accumulate(np.abs(Vh[0]).max(1))[:, None]
         assert np.all(np.abs(O[0].double().cpu().numpy() - want) <= (S.U + 2 * E) * vmax + S.U * np.abs(want))
         assert np.all(np.abs(LSE[0, 0].double().cpu().numpy() - lse) <= E + 2.0 ** -22 * np.abs(lse))
+
+
+@pytest.mark.parametrize("opts", OPTIONS, ids=NAMES)
+@pytest.mark.parametrize("mask,broken", [
+    (dict(off=[7, 75, 190, 470, 600], causal=True), None), (dict(off=[30, 331, 560], causal=False), None),
+    (dict(off=[11, 590], pre=[140], causal=True), None), (dict(off=[0, 75, 190, 470, 640], causal=True), (75, 190)),
+    (dict(off=[0, 231, 390], causal=False), (231, 390))], ids=["documents", "full", "prefix", "document", "second"])
+def test_the_bits_do_not_depend_on_time_nor_garbage(mask, broken, opts):
+    """Forward and backward with each kind of garbage in the rows of no document:
+    the same bits each time, and without a cap those that zeros there give (with
+    one the columns of a warp choose the cap's form together).  The same with
+    garbage in a document, whose rows see it."""
+    p, T, h, hkv = 2, 640, 8, 4
+    case = dict(mask, **opts)
+    rng = np.random.default_rng(5)
+    Q, K, V, dO = (S.bf16(rng, p, T, n // p * 128)[0] for n in (h, hkv, hkv, h))
+    slopes, _ = S.slopes_of(case, h)
+    offsets = mask["off"]
+    out = torch.ones(T, dtype=torch.bool, device="cuda")
+    out[offsets[0]:offsets[-1]] = False
+    if broken:
+        out[broken[0]:broken[1]] = True
+    plan = S.make_mask(offsets, mask.get("pre"), mask["causal"], T)
+    score = tp.score_params(softcap=case.get("cap", 0.0), slopes=slopes, mask=plan)
+    n = tp.tp_attention_scored_backward_workspace_size(T, p, h, hkv, 128)
+
+    def run(value):
+        x = [t.clone() for t in (Q, K, V, dO)]
+        for t in x:
+            t[:, out] = value
+        O, LSE = torch.zeros_like(Q), torch.zeros(p, h // p, T, device="cuda")
+        tp.tp_attention_scored(*x[:3], O, LSE, T, p, h, hkv, 128, score)
+        g = [torch.zeros_like(t) for t in x[:3]]
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        tp.tp_attention_scored_backward(*x[:3], O, LSE, x[3], *g, ws, n, T, p, h, hkv, 128, score)
+        tp.tp_sync_status()
+        return [t[:, ~out] for t in [O] + g] + [LSE[..., ~out]]
+
+    want = run(0.0)
+    assert all(torch.isfinite(t).all() for t in want)
+    for value in (float("nan"), float("inf"), -float("inf"), BIG, -BIG):
+        if broken or "cap" in case:
+            want = run(value)
+            assert all(torch.isfinite(t).all() for t in want)
+        for _ in range(20):
+            assert all(torch.equal(a, b) for a, b in zip(run(value), want)), value
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0, 200.0])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_visible_key_that_is_not_finite_reaches_its_queries(value, cap):
+    """dQ of the queries that see it, each time, where a mask cuts the block and
+    where none does, with O and LSE that are finite."""
+    T, key = 300, 40
+    rng = np.random.default_rng(1)
+    Q, K, V, dO = (S.bf16(rng, 1, T, 128)[0] for _ in range(4))
+    score = tp.score_params(softcap=cap, causal=True)
+    O, LSE = torch.zeros_like(Q), torch.zeros(1, 1, T, device="cuda")
+    tp.tp_attention_scored(Q, K, V, O, LSE, T, 1, 1, 1, 128, score)
+    K[0, key, 3] = value
+    n = tp.tp_attention_scored_backward_workspace_size(T, 1, 1, 1, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for _ in range(10):
+        dQ, dK, dV = (torch.zeros_like(x) for x in (Q, K, V))
+        tp.tp_attention_scored_backward(Q, K, V, O, LSE, dO, dQ, dK, dV, ws, n, T, 1, 1, 1, 128, score)
+        tp.tp_sync_status()
+        # (0 or a rounding of it times an infinity: NaN or infinite)
+        assert not torch.isfinite(dQ[0, key:, 3]).any() and torch.isfinite(dQ[0, :key]).all()
