@@ -20,7 +20,7 @@
 // that converts it.  Both are bound by a step's chain of the tensor cores' work
 // (4 and 3 products of 128 x 128 x 128 a tile, 57% and 50% of the time) and the
 // softmax's arithmetic, which overlap as far as TMEM's 512 columns allow.
-// 4096 causal tokens, 32 heads, cap: 269 and 229 us; with D, 580 in all.
+// 4096 causal tokens, 32 heads, cap: 271 and 230 us; with D, 582 in all.
 //
 // D comes from O as it was stored: dQ and dK are 0.0027 off in the 2-norm where
 // an fp32 O would leave the 0.0024 of P's, dS's and their own rounding.

@@ -20,8 +20,8 @@
 // instruction is issued only when the pipe takes it, so whatever else the
 // issuing thread does adds to the products' time (90 clocks for a commit and a
 // wait after eight of them): Q K^T and P V have a warp each, and one's waits
-// run beside the other's products.  4096 causal tokens, 64 heads, cap: 355 us,
-// 775 TFLOP/s; 2300 clocks a tile and block, of 1040 of products.
+// run beside the other's products.  4096 causal tokens, 64 heads, cap: 353 us,
+// 778 TFLOP/s; 2300 clocks a tile and block, of 1040 of products.
 // Roles (640 threads): warp 0 loads Q, K (two slots) and V (three), warp 1
 // issues Q K^T, warp 3 P V, warp 2 looks at V where a mask cuts a block, warps
 // 4..11 and 12..19 are the two softmax groups.
@@ -47,7 +47,7 @@
 // Then there is no maximum pass over the scores and O is never rescaled.  The
 // price is range: probabilities of 2^-80 to 2^80 leave V 2^128 / (2^80 T) upwards
 // and 2^-46 downwards before O's fp32 sum ends (at a cap of 50 2^56 / T and
-// 2^-54); the form with a maximum takes 395 us where this one takes 303.
+// 2^-54); the form with a maximum takes 390 to 410 us where this one takes 300.
 //
 // A key that a row does not see adds nothing to it, whatever K and V hold
 // there: its score is replaced by -inf before the softmax, and where a mask

@@ -44,7 +44,7 @@ __device__ __forceinline__ TileSpan tile_span(const MaskPlan& m, int32_t qb, int
 // Query tiles by falling number of key blocks, for units dealt to the CTAs in
 // turns from the two ends: documents of uneven length left one CTA with twice
 // the others' blocks when the tiles came in their own order (4001 tokens in
-// nine documents, 32 heads: forward 110 us, 98 sorted).  Every thread of the CTA
+// nine documents, 32 heads: forward 110 us, 98 sorted, when this was chosen).  Every thread of the CTA
 // calls this behind the wait for the plan's kernel; null where the order does
 // not matter: no mask, a unit a CTA at most, or more tiles than fit (their
 // units are many, and even out).

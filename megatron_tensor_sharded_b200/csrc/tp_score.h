@@ -134,7 +134,7 @@ cudaError_t launch_attention_mask(const LaunchCtx& c, const int32_t* off, int n_
 // SMs of a B200.
 constexpr int kScoreDkvCtas = 148;
 // A dkv unit's loads, start and stores, in steps (1999 tokens of five documents,
-// 64/8 heads, whole backward: 2 230 us, 4 226, 6 226, 8 228; a smaller one 49,
+// 64/8 heads, whole backward, when this was chosen: 2 230 us, 4 226, 6 226, 8 228; a smaller one 49,
 // 42, 41, 41).
 constexpr int kUnitCost = 4;
 int64_t score_dkv_ctas(const ScoreCall& a);
